@@ -29,6 +29,7 @@ tcclOrderAuto, tcclOrderBlocked, tcclOrderCyclic, tcclOrderDynamic = 0, 1, 2, 3
 tcclReduceAscending, tcclReduceArrival = 0, 1
 tcclLayoutAuto, tcclLayoutShared, tcclLayoutPerRank = 0, 1, 2
 TCCL_MAX_RANKS = 64
+TCCL_MAX_TOP = 128
 
 COLL_ALLREDUCE, COLL_REDUCE_SCATTER, COLL_ALLGATHER = 0, 1, 2
 
@@ -86,6 +87,12 @@ def make_layout(dims, placements, start_rank=0) -> tcclLayout_t:
     return lay
 
 
+class tcclVocab_t(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_size_t), ("vocab", ctypes.c_size_t),
+                ("shard", ctypes.c_size_t), ("row_stride", ctypes.c_size_t),
+                ("datatype", ctypes.c_int), ("temperature", ctypes.c_float)]
+
+
 def _open():
     if not LIB_PATH.exists():
         raise ImportError(f"{LIB_PATH} is missing: build it with __graft_entry__.build() "
@@ -93,6 +100,7 @@ def _open():
     lib = ctypes.CDLL(str(LIB_PATH))
     vp, pvp = ctypes.c_void_p, ctypes.POINTER(ctypes.c_void_p)
     i, sz = ctypes.c_int, ctypes.c_size_t
+    psh = ctypes.POINTER(tcclVocab_t)
     sig = {
         "tcclGetErrorString": (ctypes.c_char_p, [i]),
         "tcclGetVersion": (i, [ctypes.POINTER(i)]),
@@ -125,6 +133,10 @@ def _open():
                                    ctypes.POINTER(ctypes.c_int64), i, ctypes.POINTER(i),
                                    ctypes.POINTER(ctypes.c_int64), ctypes.POINTER(ctypes.c_int64),
                                    ctypes.POINTER(i)]),
+        "tcclLogProbs": (i, [vp, pvp, psh, vp, vp, vp, vp, i, vp, vp, vp, i]),
+        "tcclLogProbsBackward": (i, [vp, pvp, psh, vp, vp, vp, vp, vp, pvp, sz, vp, i]),
+        "tcclDistill": (i, [vp, pvp, psh, vp, vp, i, vp, i, vp, vp, vp, pvp, sz, vp, i]),
+        "tcclDistillBackward": (i, [vp, pvp, psh, vp, vp, i, vp, i, vp, vp, pvp, sz, vp, i]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -141,7 +153,8 @@ EXPORTED = ("tcclGetErrorString", "tcclGetVersion", "tcclGroupCreate", "tcclGrou
             "tcclGroupRecordSms", "tcclGroupReadSmRecord", "tcclGroupReadSmRecordLaunches",
             "tcclPlanInspect", "tcclCopyOutInspect",
             "tcclGroupInjectWaitTimeout", "tcclAllReduceNoAlloc", "tcclReshard",
-            "tcclReshardInspect", "tcclAllReduceRMSNorm")
+            "tcclReshardInspect", "tcclAllReduceRMSNorm", "tcclLogProbs", "tcclLogProbsBackward",
+            "tcclDistill", "tcclDistillBackward")
 
 
 def _ptr(x) -> int:
@@ -246,6 +259,45 @@ def tcclAllReduceRMSNorm(group, sendbufs, recvbufs, rows, hidden, gamma, eps, da
     rp, _k2 = _ptr_array(recvbufs)
     return _lib.tcclAllReduceRMSNorm(group, sp, rp, rows, hidden, _ptr(gamma), float(eps),
                                      datatype, _stream(stream), cta_cap)
+
+
+def tcclLogProbs(group, logits, shape: tcclVocab_t, tokens, log_probs, entropy=None, stats=None,
+                 top_k=0, top_log_probs=None, top_ids=None, stream=None, cta_cap=0) -> int:
+    lp, _k = _ptr_array(logits)
+    return _lib.tcclLogProbs(group, lp, ctypes.byref(shape), _ptr(tokens), _ptr(log_probs),
+                             _ptr(entropy), _ptr(stats), top_k, _ptr(top_log_probs),
+                             _ptr(top_ids), _stream(stream), cta_cap)
+
+
+def tcclLogProbsBackward(group, logits, shape: tcclVocab_t, tokens, stats, entropy, d_log_probs,
+                         d_entropy, grads, grad_stride, stream=None, cta_cap=0) -> int:
+    lp, _k1 = _ptr_array(logits)
+    gp, _k2 = _ptr_array(grads)
+    return _lib.tcclLogProbsBackward(group, lp, ctypes.byref(shape), _ptr(tokens), _ptr(stats),
+                                     _ptr(entropy), _ptr(d_log_probs), _ptr(d_entropy), gp,
+                                     grad_stride, _stream(stream), cta_cap)
+
+
+def tcclDistill(group, logits, shape: tcclVocab_t, teacher_ids, teacher_logits, teacher_datatype,
+                teacher_lse, top_k, loss, stats=None, weights=None, grads=None, grad_stride=0,
+                stream=None, cta_cap=0) -> int:
+    lp, _k1 = _ptr_array(logits)
+    gp, _k2 = _ptr_array(grads) if grads is not None else (None, None)
+    return _lib.tcclDistill(group, lp, ctypes.byref(shape), _ptr(teacher_ids),
+                            _ptr(teacher_logits), teacher_datatype, _ptr(teacher_lse), top_k,
+                            _ptr(loss), _ptr(stats), _ptr(weights), gp, grad_stride,
+                            _stream(stream), cta_cap)
+
+
+def tcclDistillBackward(group, logits, shape: tcclVocab_t, teacher_ids, teacher_logits,
+                        teacher_datatype, teacher_lse, top_k, stats, weights, grads, grad_stride,
+                        stream=None, cta_cap=0) -> int:
+    lp, _k1 = _ptr_array(logits)
+    gp, _k2 = _ptr_array(grads)
+    return _lib.tcclDistillBackward(group, lp, ctypes.byref(shape), _ptr(teacher_ids),
+                                    _ptr(teacher_logits), teacher_datatype, _ptr(teacher_lse),
+                                    top_k, _ptr(stats), _ptr(weights), gp, grad_stride,
+                                    _stream(stream), cta_cap)
 
 
 def _shape(shape):
@@ -365,6 +417,37 @@ def _dtype_code(t) -> int:
         raise TcclError(tcclInvalidArgument, f"unsupported dtype {t.dtype}") from None
 
 
+def _bad(what: str) -> TcclError:
+    return TcclError(tcclInvalidArgument, what)
+
+
+def _rank_matrices(name, mats, nranks):
+    """(rows, columns, row stride) of one matrix per rank, all alike."""
+    if len(mats) != nranks:
+        raise _bad(f"{name}: {len(mats)} tensors for {nranks} ranks")
+    first = mats[0]
+    for m in mats:
+        if m.dim() != 2 or m.shape != first.shape or m.dtype != first.dtype or not m.is_cuda:
+            raise _bad(f"{name}: needs [rows, shard] CUDA tensors of one shape and dtype")
+        # a dimension of length 1 (or an empty tensor) has a stride that says nothing
+        if m.shape[1] > 1 and m.stride(1) != 1:
+            raise _bad(f"{name}: a row's columns must be consecutive")
+        if m.shape[0] > 1 and m.stride(0) != first.stride(0):
+            raise _bad(f"{name}: every rank needs the same row stride")
+    rows, cols = first.shape
+    return rows, cols, first.stride(0) if rows > 1 else cols
+
+
+def _row_array(name, t, dtype, shape):
+    """Checks an array of one entry (or one row of entries) per row of logits."""
+    if t is None:
+        return
+    if str(t.dtype) != f"torch.{dtype}" or tuple(t.shape) != shape or not t.is_cuda or \
+            not t.is_contiguous():
+        raise _bad(f"{name}: needs a contiguous CUDA {dtype} tensor of shape {shape}, "
+                   f"got {t.dtype} {tuple(t.shape)}")
+
+
 def _current_stream():
     import torch
     return torch.cuda.current_stream().cuda_stream
@@ -459,6 +542,149 @@ class Group:
                 _stream(stream) if stream is not None else _current_stream(), cta_cap)
         return self._prepared(_lib.tcclAllReduceRMSNorm, args, "tcclAllReduceRMSNorm",
                               (keep_s, keep_r, sends, recvs, gamma))
+
+    def _vocab_shape(self, logits, vocab, temperature):
+        rows, shard, stride = _rank_matrices("logits", logits, self.nranks)
+        vocab = shard * self.nranks if vocab is None else vocab
+        if vocab < 1:
+            raise _bad(f"vocab {vocab}")
+        return tcclVocab_t(rows=rows, vocab=vocab, shard=shard, row_stride=stride,
+                           datatype=_dtype_code(logits[0]), temperature=temperature)
+
+    def _grad_stride(self, logits, grads):
+        _, _, stride = _rank_matrices("grads", grads, self.nranks)
+        if grads[0].shape != logits[0].shape or grads[0].dtype != logits[0].dtype:
+            raise _bad("grads: need the logits' shape and dtype")
+        return stride
+
+    @staticmethod
+    def _teacher(rows, teacher_ids, teacher_logits, teacher_lse):
+        if teacher_ids.dim() != 2:
+            raise _bad("teacher_ids: needs [rows, top_k]")
+        k = teacher_ids.shape[1]
+        dt = _dtype_code(teacher_logits)
+        _row_array("teacher_ids", teacher_ids, "int64", (rows, k))
+        _row_array("teacher_logits", teacher_logits, str(teacher_logits.dtype)[6:], (rows, k))
+        _row_array("teacher_lse", teacher_lse, "float32", (rows,))
+        return k, dt
+
+    def prepare_log_probs(self, logits, tokens, log_probs, entropy=None, stats=None,
+                          top_log_probs=None, top_ids=None, vocab=None, temperature=1.0,
+                          cta_cap=0, stream=None):
+        """prepare_all_reduce for log_probs."""
+        shape = self._vocab_shape(logits, vocab, temperature)
+        rows, k = shape.rows, 0
+        _row_array("tokens", tokens, "int64", (rows,))
+        _row_array("log_probs", log_probs, "float32", (rows,))
+        _row_array("entropy", entropy, "float32", (rows,))
+        _row_array("stats", stats, "float32", (rows, 2))
+        if (top_ids is None) != (top_log_probs is None):
+            raise _bad("top_ids and top_log_probs go together")
+        if top_ids is not None:
+            if top_ids.dim() != 2:
+                raise _bad("top_ids: needs [rows, top_k]")
+            k = top_ids.shape[1]
+            _row_array("top_ids", top_ids, "int64", (rows, k))
+            _row_array("top_log_probs", top_log_probs, "float32", (rows, k))
+        lp, keep = _ptr_array(logits)
+        args = (self.handle, lp, ctypes.byref(shape), _ptr(tokens), _ptr(log_probs),
+                _ptr(entropy), _ptr(stats), k, _ptr(top_log_probs), _ptr(top_ids),
+                _stream(stream) if stream is not None else _current_stream(), cta_cap)
+        return self._prepared(_lib.tcclLogProbs, args, "tcclLogProbs",
+                              (keep, shape, logits, tokens, log_probs, entropy, stats,
+                               top_log_probs, top_ids))
+
+    def prepare_log_probs_backward(self, logits, tokens, stats, d_log_probs, grads, entropy=None,
+                                   d_entropy=None, vocab=None, temperature=1.0, cta_cap=0,
+                                   stream=None):
+        """prepare_all_reduce for log_probs_backward."""
+        shape = self._vocab_shape(logits, vocab, temperature)
+        rows = shape.rows
+        _row_array("tokens", tokens, "int64", (rows,))
+        _row_array("stats", stats, "float32", (rows, 2))
+        for name, t in (("d_log_probs", d_log_probs), ("entropy", entropy), ("d_entropy", d_entropy)):
+            _row_array(name, t, "float32", (rows,))
+        lp, k1 = _ptr_array(logits)
+        gp, k2 = _ptr_array(grads)
+        args = (self.handle, lp, ctypes.byref(shape), _ptr(tokens), _ptr(stats), _ptr(entropy),
+                _ptr(d_log_probs), _ptr(d_entropy), gp, self._grad_stride(logits, grads),
+                _stream(stream) if stream is not None else _current_stream(), cta_cap)
+        return self._prepared(_lib.tcclLogProbsBackward, args, "tcclLogProbsBackward",
+                              (k1, k2, shape, logits, tokens, stats, d_log_probs, grads, entropy,
+                               d_entropy))
+
+    def prepare_distill(self, logits, teacher_ids, teacher_logits, loss, stats=None,
+                        teacher_lse=None, weights=None, grads=None, vocab=None, temperature=1.0,
+                        cta_cap=0, stream=None):
+        """prepare_all_reduce for distill."""
+        shape = self._vocab_shape(logits, vocab, temperature)
+        k, dt = self._teacher(shape.rows, teacher_ids, teacher_logits, teacher_lse)
+        _row_array("loss", loss, "float32", (shape.rows,))
+        _row_array("stats", stats, "float32", (shape.rows, 2))
+        _row_array("weights", weights, "float32", (shape.rows,))
+        lp, k1 = _ptr_array(logits)
+        gp, k2 = _ptr_array(grads) if grads is not None else (None, None)
+        args = (self.handle, lp, ctypes.byref(shape), _ptr(teacher_ids), _ptr(teacher_logits), dt,
+                _ptr(teacher_lse), k, _ptr(loss), _ptr(stats), _ptr(weights), gp,
+                self._grad_stride(logits, grads) if grads is not None else 0,
+                _stream(stream) if stream is not None else _current_stream(), cta_cap)
+        return self._prepared(_lib.tcclDistill, args, "tcclDistill",
+                              (k1, k2, shape, logits, teacher_ids, teacher_logits, loss, stats,
+                               teacher_lse, weights, grads))
+
+    def prepare_distill_backward(self, logits, teacher_ids, teacher_logits, stats, weights, grads,
+                                 teacher_lse=None, vocab=None, temperature=1.0, cta_cap=0,
+                                 stream=None):
+        """prepare_all_reduce for distill_backward."""
+        shape = self._vocab_shape(logits, vocab, temperature)
+        k, dt = self._teacher(shape.rows, teacher_ids, teacher_logits, teacher_lse)
+        _row_array("stats", stats, "float32", (shape.rows, 2))
+        _row_array("weights", weights, "float32", (shape.rows,))
+        lp, k1 = _ptr_array(logits)
+        gp, k2 = _ptr_array(grads)
+        args = (self.handle, lp, ctypes.byref(shape), _ptr(teacher_ids), _ptr(teacher_logits), dt,
+                _ptr(teacher_lse), k, _ptr(stats), _ptr(weights), gp,
+                self._grad_stride(logits, grads),
+                _stream(stream) if stream is not None else _current_stream(), cta_cap)
+        return self._prepared(_lib.tcclDistillBackward, args, "tcclDistillBackward",
+                              (k1, k2, shape, logits, teacher_ids, teacher_logits, stats, weights,
+                               grads, teacher_lse))
+
+    def log_probs(self, logits, tokens, log_probs, entropy=None, stats=None, top_log_probs=None,
+                  top_ids=None, vocab=None, temperature=1.0, cta_cap=0, stream=None):
+        """log_probs[t] = the log probability of tokens[t] under row t of the
+        vocabulary-parallel logits (one [rows, shard] tensor per rank; columns
+        past `vocab` are padding), with its entropy and its top_ids.shape[1]
+        best columns where those tensors are given (see tcclLogProbs)."""
+        self.prepare_log_probs(logits, tokens, log_probs, entropy, stats, top_log_probs, top_ids,
+                               vocab, temperature, cta_cap, stream)()
+        return log_probs
+
+    def log_probs_backward(self, logits, tokens, stats, d_log_probs, grads, entropy=None,
+                           d_entropy=None, vocab=None, temperature=1.0, cta_cap=0, stream=None):
+        """grads[r] = the logits' gradient of sum_t (d_log_probs[t] log_probs[t]
+        + d_entropy[t] entropy[t]), from the forward's stats and entropy (see
+        tcclLogProbsBackward). grads may be the logits themselves."""
+        self.prepare_log_probs_backward(logits, tokens, stats, d_log_probs, grads, entropy,
+                                        d_entropy, vocab, temperature, cta_cap, stream)()
+        return grads
+
+    def distill(self, logits, teacher_ids, teacher_logits, loss, stats=None, teacher_lse=None,
+                weights=None, grads=None, vocab=None, temperature=1.0, cta_cap=0, stream=None):
+        """loss[t] = the divergence of the vocabulary-parallel logits' row t from
+        a teacher's top entries; with weights and grads also the gradient of
+        sum_t weights[t] loss[t], in the same pass (see tcclDistill)."""
+        self.prepare_distill(logits, teacher_ids, teacher_logits, loss, stats, teacher_lse,
+                             weights, grads, vocab, temperature, cta_cap, stream)()
+        return loss
+
+    def distill_backward(self, logits, teacher_ids, teacher_logits, stats, weights, grads,
+                         teacher_lse=None, vocab=None, temperature=1.0, cta_cap=0, stream=None):
+        """grads[r] = the logits' gradient of sum_t weights[t] loss[t] of
+        distill, from its stats (see tcclDistillBackward)."""
+        self.prepare_distill_backward(logits, teacher_ids, teacher_logits, stats, weights, grads,
+                                      teacher_lse, vocab, temperature, cta_cap, stream)()
+        return grads
 
     def all_reduce(self, sends, recvs=None, op="sum", cta_cap=0, stream=None):
         """recvs[r] = fold over ranks of sends (ascending rank order). With

@@ -18,10 +18,11 @@ INCLUDE = ROOT / "include"
 LIB = PKG / "libtccl.so"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
-HOST_SOURCES = ["api.cpp", "plan.cpp", "reshard.cpp", "copy_out_host.cpp"]
+HOST_SOURCES = ["api.cpp", "plan.cpp", "reshard.cpp", "copy_out_host.cpp",
+                "vocab_host.cpp"]
 CUDA_SOURCES = ["kernels_bulk.cu", "kernels_small_ar.cu", "kernels_small_rs.cu",
                 "kernels_small_ag.cu", "kernels_reshard.cu", "kernels_rmsnorm.cu",
-                "no_alloc.cu", "kernels_copy_out.cu"]
+                "no_alloc.cu", "kernels_copy_out.cu", "kernels_vocab.cu"]
 
 
 def _cuda_home() -> Path:

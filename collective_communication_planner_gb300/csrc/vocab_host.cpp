@@ -1,0 +1,254 @@
+// C entry points of the operators over vocabulary-parallel logits
+// (include/tccl.h): argument validation and launches. Host code only; the
+// kernels are in kernels_vocab.cu.
+#include "vocab.h"
+
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstring>
+
+#include "group.h"
+#include "tccl.h"
+
+using namespace tccl;
+
+namespace {
+
+// `rows` rows of `width` bytes, `stride` bytes apart
+struct Block {
+  uintptr_t at;
+  uint64_t rows, width, stride;
+  uint64_t span() const { return rows ? (rows - 1) * stride + width : 0; }
+};
+
+bool overlap(const Block& a, const Block& b) {
+  if (!a.span() || !b.span()) return false;
+  if (a.at >= b.at + b.span() || b.at >= a.at + a.span()) return false;
+  // column blocks of one matrix interleave without touching: with equal
+  // strides and b starting `d` bytes into a's stride, b's rows lie in the
+  // gaps between a's
+  if (a.stride != b.stride || a.rows == 1 || b.rows == 1) return true;
+  const uint64_t d = a.at <= b.at ? (b.at - a.at) % a.stride
+                                  : (a.stride - (a.at - b.at) % a.stride) % a.stride;
+  return d < a.width || d + b.width > a.stride;
+}
+
+Block vec(const void* p, uint64_t bytes) { return Block{(uintptr_t)p, 1, bytes, bytes}; }
+
+// The arrays of one call: inputs, then outputs, checked against one another.
+class Arrays {
+ public:
+  // false: null or misaligned
+  bool in(const void* p, uint64_t bytes, size_t align) { return add(p, bytes, align, false); }
+  bool out(const void* p, uint64_t bytes, size_t align) { return add(p, bytes, align, true); }
+  bool disjoint(const Block* logits, const Block* grads, int n) const {
+    for (int i = 0; i < n_; ++i) {
+      for (int k = 0; k < i; ++k)
+        if ((is_out_[i] || is_out_[k]) && overlap(block_[i], block_[k])) return false;
+      for (int r = 0; r < n; ++r) {
+        if (is_out_[i] && overlap(block_[i], logits[r])) return false;
+        if (grads && overlap(block_[i], grads[r])) return false;
+      }
+    }
+    if (!grads) return true;
+    for (int r = 0; r < n; ++r)
+      for (int k = 0; k < n; ++k) {
+        const bool in_place = k == r && grads[r].at == logits[r].at && grads[r].stride == logits[r].stride;
+        if (!in_place && overlap(grads[r], logits[k])) return false;
+        if (k != r && overlap(grads[r], grads[k])) return false;
+      }
+    return true;
+  }
+
+ private:
+  bool add(const void* p, uint64_t bytes, size_t align, bool out) {
+    if (!p || (uintptr_t)p % align) return false;
+    block_[n_] = vec(p, bytes);
+    is_out_[n_++] = out;
+    return true;
+  }
+  Block block_[8];
+  bool is_out_[8];
+  int n_ = 0;
+};
+
+// Fills the argument block of a call on `shape`; grads may be null.
+bool fill(tcclGroup* g, const void* const* logits, const tcclVocab_t* shape, void* const* grads,
+          size_t grad_stride, VocabArgs* v, Block* src, Block* dst) {
+  if (!logits || !shape) return false;
+  if (shape->datatype != tcclFloat32 && shape->datatype != tcclBfloat16) return false;
+  if (!(shape->temperature >= 1.f / 1024 && shape->temperature <= 1024.f)) return false;
+  const uint64_t limit = (uint64_t)1 << 31;
+  if (shape->rows >= limit || shape->shard == 0 || shape->shard >= limit ||
+      shape->shard * (uint64_t)g->nranks >= limit)
+    return false;
+  if (shape->vocab == 0 || shape->vocab > shape->shard * (uint64_t)g->nranks) return false;
+  // strides bounded so that no byte offset passes 64 bits
+  if (shape->row_stride < shape->shard || shape->row_stride >= limit) return false;
+  if (grads && (grad_stride < shape->shard || grad_stride >= limit)) return false;
+  const size_t es = shape->datatype == tcclBfloat16 ? 2 : 4;
+  std::memset(v, 0, sizeof(*v));
+  for (int r = 0; r < g->nranks; ++r) {
+    if ((!logits[r] && shape->rows) || (uintptr_t)logits[r] % es) return false;
+    src[r] = Block{(uintptr_t)logits[r], shape->rows, shape->shard * es, shape->row_stride * es};
+    v->p.src[r] = logits[r];
+    if (!grads) continue;
+    if ((!grads[r] && shape->rows) || (uintptr_t)grads[r] % es) return false;
+    dst[r] = Block{(uintptr_t)grads[r], shape->rows, shape->shard * es, grad_stride * es};
+    v->p.dst[r] = grads[r];
+  }
+  v->rows = shape->rows;
+  v->src_stride = shape->row_stride;
+  v->dst_stride = grad_stride;
+  v->vocab = (uint32_t)shape->vocab;
+  v->shard = (uint32_t)shape->shard;
+  v->nranks = g->nranks;
+  v->used = (int)((shape->vocab + shape->shard - 1) / shape->shard);
+  v->inv_temp = (float)(1.0 / (double)shape->temperature);
+  v->exp2_scale = (float)(1.4426950408889634 / (double)shape->temperature);
+  return true;
+}
+
+// Launches on the group's device and notes the launch shape.
+template <typename Args>
+tcclResult_t run(tcclGroup* g, int (*launch)(int, const Args&, int, int, int*, int*, void*), Args& a,
+                 int dtype, int cap, cudaStream_t stream) {
+  int cur = -1;
+  if (cudaGetDevice(&cur) != cudaSuccess) return tcclCudaError;
+  if (cur != g->device && cudaSetDevice(g->device) != cudaSuccess) return tcclCudaError;
+  a.v.sm_mask = sm_record_slot(g);
+  std::memset(&g->last, 0, sizeof(g->last));
+  const int err = launch(dtype, a, g->dev.sm_count, cap, &g->last.ctas, &g->last.threads, stream);
+  if (cur != g->device) cudaSetDevice(cur);
+  return err == 0 ? tcclSuccess : tcclCudaError;
+}
+
+}  // namespace
+
+extern "C" {
+
+tcclResult_t tcclLogProbs(tcclGroup_t g, const void* const logits[], const tcclVocab_t* shape,
+                          const int64_t* tokens, float* log_probs, float* entropy, float* stats,
+                          int top_k, float* top_log_probs, int64_t* top_ids, cudaStream_t stream,
+                          int cta_cap) {
+  if (!g) return tcclInvalidArgument;
+  LogProbsArgs a;
+  Block src[kMaxRanks];
+  if (!fill(g, logits, shape, nullptr, 0, &a.v, src, nullptr)) return tcclInvalidArgument;
+  if (top_k < 0 || top_k > TCCL_MAX_TOP || !tokens != !log_probs) return tcclInvalidArgument;
+  const uint64_t n = shape->rows;
+  if (n == 0) return tcclSuccess;  // empty arrays may be null
+  Arrays x;
+  if (tokens && (!x.in(tokens, n * 8, 8) || !x.out(log_probs, n * 4, 4))) return tcclInvalidArgument;
+  if (entropy && !x.out(entropy, n * 4, 4)) return tcclInvalidArgument;
+  if (stats && !x.out(stats, n * 8, 4)) return tcclInvalidArgument;
+  if (top_k && (!x.out(top_log_probs, n * 4 * top_k, 4) || !x.out(top_ids, n * 8 * top_k, 8)))
+    return tcclInvalidArgument;
+  if (!x.disjoint(src, nullptr, g->nranks)) return tcclInvalidArgument;
+  a.tokens = tokens;
+  a.log_probs = log_probs;
+  a.entropy = entropy;
+  a.stats = stats;
+  a.top_log_probs = top_log_probs;
+  a.top_ids = top_ids;
+  a.top_k = top_k;
+  return run(g, launch_log_probs, a, shape->datatype, cta_cap, stream);
+}
+
+tcclResult_t tcclLogProbsBackward(tcclGroup_t g, const void* const logits[],
+                                  const tcclVocab_t* shape, const int64_t* tokens,
+                                  const float* stats, const float* entropy,
+                                  const float* d_log_probs, const float* d_entropy,
+                                  void* const grads[], size_t grad_stride, cudaStream_t stream,
+                                  int cta_cap) {
+  if (!g || !grads) return tcclInvalidArgument;
+  LogProbsGradArgs a;
+  Block src[kMaxRanks], dst[kMaxRanks];
+  if (!fill(g, logits, shape, grads, grad_stride, &a.v, src, dst)) return tcclInvalidArgument;
+  const uint64_t n = shape->rows;
+  if (n == 0) return tcclSuccess;  // empty arrays may be null
+  Arrays x;
+  if (!x.in(tokens, n * 8, 8) || !x.in(stats, n * 8, 4) || !x.in(d_log_probs, n * 4, 4))
+    return tcclInvalidArgument;
+  if (d_entropy && (!x.in(d_entropy, n * 4, 4) || !x.in(entropy, n * 4, 4))) return tcclInvalidArgument;
+  if (!x.disjoint(src, dst, g->nranks)) return tcclInvalidArgument;
+  a.tokens = tokens;
+  a.stats = stats;
+  a.entropy = d_entropy ? entropy : nullptr;
+  a.d_log_probs = d_log_probs;
+  a.d_entropy = d_entropy;
+  return run(g, launch_log_probs_grad, a, shape->datatype, cta_cap, stream);
+}
+
+namespace {
+
+// What both distillation calls check and set.
+bool fill_teacher(const tcclVocab_t* shape, const int64_t* ids, const void* teacher,
+                  tcclDataType_t teacher_datatype, const float* teacher_lse, int top_k, Arrays* x,
+                  DistillArgs* a) {
+  if (teacher_datatype != tcclFloat32 && teacher_datatype != tcclBfloat16) return false;
+  if (top_k < 1 || top_k > TCCL_MAX_TOP) return false;
+  const uint64_t n = shape->rows;
+  const size_t es = teacher_datatype == tcclBfloat16 ? 2 : 4;
+  if (!x->in(ids, n * 8 * top_k, 8) || !x->in(teacher, n * es * top_k, es)) return false;
+  if (teacher_lse && !x->in(teacher_lse, n * 4, 4)) return false;
+  a->ids = ids;
+  a->teacher = teacher;
+  a->teacher_lse = teacher_lse;
+  a->top_k = top_k;
+  a->teacher_bf16 = teacher_datatype == tcclBfloat16;
+  a->loss = a->stats = nullptr;
+  a->weights = a->saved = nullptr;
+  return true;
+}
+
+}  // namespace
+
+tcclResult_t tcclDistill(tcclGroup_t g, const void* const logits[], const tcclVocab_t* shape,
+                         const int64_t* teacher_ids, const void* teacher_logits,
+                         tcclDataType_t teacher_datatype, const float* teacher_lse, int top_k,
+                         float* loss, float* stats, const float* weights, void* const grads[],
+                         size_t grad_stride, cudaStream_t stream, int cta_cap) {
+  if (!g) return tcclInvalidArgument;
+  DistillArgs a;
+  Block src[kMaxRanks], dst[kMaxRanks];
+  if (!fill(g, logits, shape, grads, grad_stride, &a.v, src, dst)) return tcclInvalidArgument;
+  const uint64_t n = shape->rows;
+  if (n == 0) return tcclSuccess;
+  Arrays x;
+  if (!fill_teacher(shape, teacher_ids, teacher_logits, teacher_datatype, teacher_lse, top_k, &x, &a))
+    return tcclInvalidArgument;
+  if (!weights != !grads) return tcclInvalidArgument;
+  if (!x.out(loss, n * 4, 4) || (stats && !x.out(stats, n * 8, 4))) return tcclInvalidArgument;
+  if (weights && !x.in(weights, n * 4, 4)) return tcclInvalidArgument;
+  if (!x.disjoint(src, grads ? dst : nullptr, g->nranks)) return tcclInvalidArgument;
+  a.loss = loss;
+  a.stats = stats;
+  a.weights = weights;
+  return run(g, launch_distill, a, shape->datatype, cta_cap, stream);
+}
+
+tcclResult_t tcclDistillBackward(tcclGroup_t g, const void* const logits[],
+                                 const tcclVocab_t* shape, const int64_t* teacher_ids,
+                                 const void* teacher_logits, tcclDataType_t teacher_datatype,
+                                 const float* teacher_lse, int top_k, const float* stats,
+                                 const float* weights, void* const grads[], size_t grad_stride,
+                                 cudaStream_t stream, int cta_cap) {
+  if (!g || !grads) return tcclInvalidArgument;
+  DistillArgs a;
+  Block src[kMaxRanks], dst[kMaxRanks];
+  if (!fill(g, logits, shape, grads, grad_stride, &a.v, src, dst)) return tcclInvalidArgument;
+  const uint64_t n = shape->rows;
+  if (n == 0) return tcclSuccess;
+  Arrays x;
+  if (!fill_teacher(shape, teacher_ids, teacher_logits, teacher_datatype, teacher_lse, top_k, &x, &a))
+    return tcclInvalidArgument;
+  if (!x.in(stats, n * 8, 4) || !x.in(weights, n * 4, 4)) return tcclInvalidArgument;
+  if (!x.disjoint(src, dst, g->nranks)) return tcclInvalidArgument;
+  a.saved = stats;
+  a.weights = weights;
+  return run(g, launch_distill_grad, a, shape->datatype, cta_cap, stream);
+}
+
+}  // extern "C"

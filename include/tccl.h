@@ -459,6 +459,119 @@ tcclResult_t tcclReshardInspect(const tcclLayout_t* src, const tcclLayout_t* dst
                                 int64_t* bytes_read, int64_t* bytes_written, int* n_windows);
 
 /*
+ * Operators over vocabulary-parallel logits: log probabilities of given
+ * tokens with entropy and the top alternatives, and distillation from a
+ * teacher's top logits, each with its gradient. They have no counterpart on
+ * the pages: they are what follows a tensor-parallel model's last allreduce
+ * and head product, whose logits the P ranks hold cut by columns.
+ *
+ * Rank r's buffer holds columns [r * shard, (r + 1) * shard) of every row,
+ * fp32 or bf16, consecutive in memory, rows row_stride elements apart.
+ * Columns at or past `vocab` are padding: never read as logits, and their
+ * gradient is written as zero. Buffers need the alignment of their elements
+ * only (16-byte aligned ones with strides and shards of whole 16-byte vectors
+ * are fastest), and may be column blocks of one matrix. With x a row's valid
+ * columns:
+ *   z_j = x_j / temperature, lse = log sum_j exp(z_j), p_j = exp(z_j - lse).
+ * Sums are kept in fp32 from one pass with a running maximum; nothing is
+ * rounded to the datatype but the gradients, once. No call uses floating-point
+ * atomics: the same call gives the same bits.
+ *
+ * A row's statistics, which a forward call writes and a gradient call reads,
+ * are two floats: stats[2 t] = max_j x_j and
+ * stats[2 t + 1] = log sum_j exp(z_j - max z), so lse = stats[2 t] /
+ * temperature + stats[2 t + 1]. A row whose columns are all -inf (a mask that
+ * leaves nothing) has stats (-inf, 0) and gradient zero. A row holding NaN or
+ * +inf has NaN results.
+ *
+ * Arrays without a rank index are in device memory, contiguous, one entry (or
+ * top_k entries) per row; all pointer rules of this header hold. An output may
+ * overlap no other array, except grads[r] == logits[r] with the same stride
+ * (in place). A cta_cap > 0 bounds the CTAs; rows == 0 returns without a
+ * launch. Errors: tcclInvalidArgument for a null or misaligned pointer, an
+ * integer datatype, vocab outside [1, nranks * shard], a stride below shard,
+ * rows, nranks * shard or a stride of 2^31 or more, temperature outside
+ * [1/1024, 1024], a top_k out of range or a forbidden overlap.
+ */
+#define TCCL_MAX_TOP 128
+typedef struct {
+  size_t rows;
+  size_t vocab;            /* columns that count, over all ranks */
+  size_t shard;            /* columns of one rank */
+  size_t row_stride;       /* elements from a row to the next, in every logits buffer */
+  tcclDataType_t datatype; /* tcclFloat32 or tcclBfloat16: logits and gradients */
+  float temperature;
+} tcclVocab_t;
+
+/*
+ * For every row t with token j = tokens[t] in [0, vocab):
+ *   log_probs[t] = z_j - lse (-inf where x_j is),
+ *   entropy[t]   = -sum_j p_j log p_j (0 for a row all -inf),
+ *   stats        as above,
+ *   top_ids[t * top_k + i], top_log_probs[t * top_k + i], i < top_k: the i-th
+ *   column by value, larger first, the lower column first among equals, and
+ *   its log probability; past the last column above -inf: id -1, -inf. A row
+ *   holding NaN or +inf: ids -1, NaN.
+ * A token outside [0, vocab) marks a row that is not scored: it is not read,
+ * its results are 0 and its alternatives -1 and -inf. With tokens (and
+ * log_probs) null every row is read and only the other results are written.
+ * entropy, stats and (for top_k == 0) the alternatives may be null;
+ * 0 <= top_k <= TCCL_MAX_TOP.
+ */
+tcclResult_t tcclLogProbs(tcclGroup_t g, const void* const logits[], const tcclVocab_t* shape,
+                          const int64_t* tokens, float* log_probs, float* entropy, float* stats,
+                          int top_k, float* top_log_probs, int64_t* top_ids, cudaStream_t stream,
+                          int cta_cap);
+
+/*
+ * The gradient of tcclLogProbs: with a = d_log_probs[t], b = d_entropy[t],
+ *   grads[.][t, j] = (a [j == token] - p_j (a + b (log p_j + entropy[t]))) / temperature.
+ * stats and entropy are the forward's; d_entropy (and entropy) may be null,
+ * b = 0 then. Rows grad_stride elements apart. A row that is not scored, or
+ * whose a and b are both 0, is not read and gets zeros.
+ */
+tcclResult_t tcclLogProbsBackward(tcclGroup_t g, const void* const logits[],
+                                  const tcclVocab_t* shape, const int64_t* tokens,
+                                  const float* stats, const float* entropy,
+                                  const float* d_log_probs, const float* d_entropy,
+                                  void* const grads[], size_t grad_stride, cudaStream_t stream,
+                                  int cta_cap);
+
+/*
+ * Distillation from the top_k logits a teacher kept of each row,
+ * teacher_ids[t * top_k + k] and teacher_logits (teacher_datatype, fp32 or
+ * bf16) the same way; 1 <= top_k <= TCCL_MAX_TOP. With q the softmax of
+ * teacher_logits[t] / temperature over the row's entries, or, with
+ * teacher_lse given (the log-sum-exp of the teacher's whole row at that
+ * temperature), q_k = exp(teacher_logits / temperature - teacher_lse[t]),
+ *   loss[t] = sum_k q_k (log q_k - log p[id_k]).
+ * An entry whose id is outside [0, vocab) or whose logit is -inf is empty; a
+ * row of empty entries has loss 0. Entries that name one column twice add up.
+ * With weights and grads (both or neither) the gradient of sum_t weights[t]
+ * loss[t] is written too, with Q = sum_k q_k:
+ *   grads[.][t, j] = weights[t] (Q p_j - sum_{k: id_k = j} q_k) / temperature,
+ * zeros where weights[t] is 0. stats may be null. Cross entropy with its
+ * gradient is top_k = 1: the label, with any finite teacher logit.
+ */
+tcclResult_t tcclDistill(tcclGroup_t g, const void* const logits[], const tcclVocab_t* shape,
+                         const int64_t* teacher_ids, const void* teacher_logits,
+                         tcclDataType_t teacher_datatype, const float* teacher_lse, int top_k,
+                         float* loss, float* stats, const float* weights, void* const grads[],
+                         size_t grad_stride, cudaStream_t stream, int cta_cap);
+
+/*
+ * The gradient of tcclDistill alone, from the forward's stats, where the
+ * weights are only known after the loss. A row with weight 0, or without
+ * entries, is not read and gets zeros.
+ */
+tcclResult_t tcclDistillBackward(tcclGroup_t g, const void* const logits[],
+                                 const tcclVocab_t* shape, const int64_t* teacher_ids,
+                                 const void* teacher_logits, tcclDataType_t teacher_datatype,
+                                 const float* teacher_lse, int top_k, const float* stats,
+                                 const float* weights, void* const grads[], size_t grad_stride,
+                                 cudaStream_t stream, int cta_cap);
+
+/*
  * Allreduce for callers that cannot allocate GPU memory (no counterpart in
  * the paper: a convenience of this library).
  *
