@@ -1,0 +1,452 @@
+// Forward passes over vocabulary-parallel logits: log probabilities with
+// entropy and top alternatives, and the distillation loss.
+#include "vocab_device.cuh"
+
+namespace tccl {
+namespace {
+
+using namespace vocab;
+
+constexpr int kThreads = 256;
+constexpr int kBatch = 4;          // vectors a thread loads together
+constexpr int kMaxEntries = 64;    // stored batch maxima per thread
+constexpr int kMaxWork = 512;      // batches looked at again for alternatives
+constexpr int kMaxCandidates = 1024;
+constexpr int kForwardCluster = 8;
+
+// Adds a batch to a thread's part: the largest element first, then the sums.
+template <int DT>
+__device__ __forceinline__ float add_batch(Part& a, float& r, f32x2 (&s)[2], f32x2 (&u)[2], Vec<DT> (&x)[kBatch], float c) {
+#pragma unroll
+  for (int k = 0; k < kBatch; ++k) x[k].clamp();
+  const float top = batch_max<DT, kBatch>(x);
+  if (top > a.m) {
+    const float to = __fmul_rn(top, c), d = __fsub_rn(r, to), f = exp2_ftz(d);
+    const f32x2 dd = pack(d, d), ff = pack(f, f);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      // d may be -inf only where f is 0 and s is 0 or vanishes
+      u[i] = f == 0.f ? 0ull : mul2(ff, fma2(s[i], dd, u[i]));
+      s[i] = f == 0.f ? 0ull : mul2(ff, s[i]);
+    }
+    a.m = top;
+    r = to;
+  }
+  const f32x2 cc = pack(c, c), rr = pack(-r, -r);
+#pragma unroll
+  for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+    for (int i = 0; i < Vec<DT>::kPairs; ++i) {
+      const f32x2 d = fma2(x[k].pair(i), cc, rr);
+      const f32x2 e = exp2x2(d);
+      s[i & 1] = add2(s[i & 1], e);
+      u[i & 1] = fma2(e, d, u[i & 1]);
+    }
+  return top;
+}
+
+// The smallest bf16 number that is not below x, as its bits.
+__device__ __forceinline__ uint16_t bf16_above(float x) {
+  const uint32_t b = __float_as_uint(x);
+  return static_cast<uint16_t>((b & 0x80000000u) ? b >> 16 : (b + 0xFFFFu) >> 16);
+}
+
+// This thread's part of vectors [lo, hi) of the row, and of its edge elements
+// where `edges` is set.
+// With TOP, the maximum of every 2^shift batches is kept in `tops`, for the
+// alternatives.
+template <int DT, bool TOP>
+__device__ __forceinline__ Part scan_row(const VocabArgs& v, const Segments& seg, uint32_t lo, uint32_t hi,
+                                         bool edges, uint16_t* tops, int shift) {
+  const float c = v.exp2_scale;
+  Part a{kClamp, 0.f, 0.f};
+  float r = __fmul_rn(kClamp, c);
+  f32x2 s[2] = {0, 0}, u[2] = {0, 0};
+  int batch = 0;
+  float entry = kClamp;
+  for (Walk w(v.cut, lo + threadIdx.x); w.index < hi;) {
+    Vec<DT> x[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (w.index < hi) x[k].set(dev::ld_global_v4(seg.at<DT>(w.seg, seg.head[w.seg] + w.vec * Elem<DT>::kVec)));
+      else x[k].set_empty();
+      w.next(v.cut);
+    }
+    const float top = add_batch<DT>(a, r, s, u, x, c);
+    if (TOP) {
+      entry = fmaxf(entry, top);
+      if ((++batch & ((1 << shift) - 1)) == 0 || w.index >= hi) {
+        tops[((batch - 1) >> shift) * kThreads + threadIdx.x] = bf16_above(entry);
+        entry = kClamp;
+      }
+    }
+  }
+  float s0, s1, s2, s3;
+  unpack(s[0], s0, s1);
+  unpack(s[1], s2, s3);
+  a.s = (s0 + s1) + (s2 + s3);
+  unpack(u[0], s0, s1);
+  unpack(u[1], s2, s3);
+  a.u = (s0 + s1) + (s2 + s3);
+  for (uint32_t e = threadIdx.x; edges && e < v.cut.edges; e += kThreads) {
+    uint32_t es, col;
+    edge_at<DT>(v, seg, e, es, col);
+    const float x = max_f32(load_one<DT>(seg.at<DT>(es, col)), kClamp);
+    if (x > a.m) rebase(a, x, c);
+    const float d = __fmaf_rn(x, c, -__fmul_rn(a.m, c)), p = exp2_ftz(d);
+    a.s += p;
+    a.u = __fmaf_rn(p, d, a.u);
+  }
+  return a;
+}
+
+template <int DT, bool TOP>
+__device__ __forceinline__ Stats row_stats(const VocabArgs& v, const Segments& seg, uint32_t lo, uint32_t hi,
+                                           uint32_t cta, uint32_t ctas, JoinSlots& slots, int& phase,
+                                           uint16_t* tops, int shift, float& thread_max) {
+  Part a = scan_row<DT, TOP>(v, seg, lo, hi, cta == 0, tops, shift);
+  thread_max = a.m;
+  a = row_join(a, v.exp2_scale, slots, phase, ctas);
+  if (fabsf(a.m) < -kClamp) return stats_of(a, v.exp2_scale);
+  return slow_stats<DT>(v, seg, lo, hi, slots, phase, cta, ctas);
+}
+
+// ---------------------------------------------------------------- alternatives
+// A value and its column as one number that orders alternatives: larger
+// values first, the lower column first among equals. 0: no alternative (-inf).
+__device__ __forceinline__ uint32_t order_of(float x) {
+  const uint32_t b = __float_as_uint(x + 0.f);  // -0 counts as 0
+  return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ uint64_t key_of(float x, uint32_t column) {
+  if (!(x > -INFINITY)) return 0;
+  return static_cast<uint64_t>(order_of(x)) << 32 | (0xFFFFFFFFu - column);
+}
+__device__ __forceinline__ float key_value(uint64_t k) {
+  const uint32_t o = static_cast<uint32_t>(k >> 32);
+  return __uint_as_float((o & 0x80000000u) ? o & 0x7FFFFFFFu : ~o);
+}
+__device__ __forceinline__ int64_t key_column(uint64_t k) {
+  return static_cast<int64_t>(0xFFFFFFFFu - static_cast<uint32_t>(k));
+}
+
+struct TopSlots {
+  uint64_t candidate[kMaxCandidates];
+  uint64_t sorted[kMaxTop];
+  uint32_t order[kThreads];  // every thread's maximum
+  uint32_t work[kMaxWork];   // entry * kThreads + thread
+  int candidates, works;
+  float threshold;
+  int found;
+};
+
+__device__ __forceinline__ void offer(TopSlots& t, float x, uint32_t column) {
+  const uint64_t k = key_of(x, column);
+  if (!k) return;
+  const int i = atomicAdd(&t.candidates, 1);
+  if (i < kMaxCandidates) t.candidate[i] = k;
+}
+
+// The best k of the first n candidates, sorted, into t.sorted; t.found of
+// them. Keys differ, so a key's place is the number of larger ones. All threads.
+__device__ void sort_candidates(TopSlots& t, int n, int k) {
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const uint64_t mine = t.candidate[i];
+    int place = 0;
+    for (int j = 0; j < n; ++j) place += t.candidate[j] > mine;
+    if (place < k) t.sorted[place] = mine;
+  }
+  if (threadIdx.x == 0) t.found = min(n, k);
+  __syncthreads();
+}
+
+// The same for any row, one element a thread and step: keeps the best k so far
+// and drops what is below the k-th whenever the list is nearly full.
+template <int DT>
+__device__ __noinline__ void select_by_scan(const VocabArgs& v, const Segments& seg, uint32_t lo, uint32_t hi,
+                                            bool edges, TopSlots& t, int k) {
+  constexpr int K = Elem<DT>::kVec;
+  __syncthreads();
+  if (threadIdx.x == 0) t.candidates = 0;
+  uint64_t floor_key = 0;
+  const auto prune = [&](bool last) {
+    __syncthreads();
+    const int n = t.candidates;
+    if (!last && n <= kMaxCandidates - kThreads) {
+      __syncthreads();  // nobody adds before everybody has read
+      return;
+    }
+    sort_candidates(t, n, k);
+    if (!last) {
+      if (t.found == k) floor_key = t.sorted[k - 1];
+      for (int i = threadIdx.x; i < t.found; i += kThreads) t.candidate[i] = t.sorted[i];
+      if (threadIdx.x == 0) t.candidates = t.found;
+      __syncthreads();
+    }
+  };
+  const auto take = [&](bool on, float x, uint32_t column) {
+    if (on && key_of(x, column) > floor_key) offer(t, x, column);
+    prune(false);
+  };
+  __syncthreads();
+  const uint32_t steps = (hi - lo + kThreads - 1) / kThreads;
+  Walk w(v.cut, lo + threadIdx.x);
+  for (uint32_t i = 0; i < steps; ++i, w.next(v.cut)) {
+    const bool on = w.index < hi;
+    const uint32_t col = on ? seg.head[w.seg] + w.vec * K : 0;
+    for (int j = 0; j < K; ++j)
+      take(on, on ? load_one<DT>(seg.at<DT>(w.seg, col + j)) : 0.f, w.seg * v.shard + col + j);
+  }
+  for (uint32_t e0 = 0; edges && e0 < v.cut.edges; e0 += kThreads) {
+    const uint32_t e = e0 + threadIdx.x;
+    const bool on = e < v.cut.edges;
+    uint32_t es = 0, col = 0;
+    if (on) edge_at<DT>(v, seg, e, es, col);
+    take(on, on ? load_one<DT>(seg.at<DT>(es, col)) : 0.f, es * v.shard + col);
+  }
+  prune(true);
+}
+
+// The best k columns among this CTA's vectors [lo, hi) and edge elements,
+// sorted, in t.sorted[0 .. t.found). The k-th largest of the threads' maxima
+// is at most the k-th largest element, so only batches whose maximum reaches
+// it are read again.
+template <int DT>
+__device__ void select_top(const VocabArgs& v, const Segments& seg, uint32_t lo, uint32_t hi, bool edges,
+                           TopSlots& t, int k, const uint16_t* tops, int shift,
+                           float thread_max, bool slow) {
+  constexpr int K = Elem<DT>::kVec;
+  if (slow) {  // the maxima were clamped
+    select_by_scan<DT>(v, seg, lo, hi, edges, t, k);
+    return;
+  }
+  const uint32_t mine = order_of(thread_max);
+  t.order[threadIdx.x] = mine;
+  if (threadIdx.x == 0) t.candidates = t.works = 0;
+  __syncthreads();
+  int place = 0;
+  const uint4* all = reinterpret_cast<const uint4*>(t.order);
+#pragma unroll 4
+  for (int i = 0; i < kThreads / 4; ++i) {
+    const uint4 o = all[i];
+    const int j = 4 * i, me = threadIdx.x;
+    place += (o.x > mine || (o.x == mine && j < me)) + (o.y > mine || (o.y == mine && j + 1 < me)) +
+             (o.z > mine || (o.z == mine && j + 2 < me)) + (o.w > mine || (o.w == mine && j + 3 < me));
+  }
+  if (place == k - 1) t.threshold = thread_max;
+  __syncthreads();
+  // at the clamp: too few threads have an element above it, any element counts
+  const float threshold = t.threshold > kClamp ? t.threshold : -INFINITY;
+  const int entries = lo + threadIdx.x < hi
+      ? (((hi - lo - threadIdx.x + kThreads - 1) / kThreads + kBatch - 1) / kBatch + (1 << shift) - 1) >> shift : 0;
+  for (int i = 0; i < entries; ++i) {
+    if (__uint_as_float(static_cast<uint32_t>(tops[i * kThreads + threadIdx.x]) << 16) >= threshold) {
+      const int n = atomicAdd(&t.works, 1);
+      if (n < kMaxWork) t.work[n] = i * kThreads + threadIdx.x;
+    }
+  }
+  for (uint32_t e = threadIdx.x; edges && e < v.cut.edges; e += kThreads) {
+    uint32_t es, col;
+    edge_at<DT>(v, seg, e, es, col);
+    const float x = load_one<DT>(seg.at<DT>(es, col));
+    if (x >= threshold) offer(t, x, es * v.shard + col);
+  }
+  __syncthreads();
+  if (t.works <= kMaxWork) {
+    const int per = kBatch << shift, items = t.works * per;
+    for (int i = threadIdx.x; i < items; i += kThreads) {
+      const uint32_t job = t.work[i / per];
+      const uint32_t index = lo + (job / kThreads * per + i % per) * kThreads + job % kThreads;
+      if (index >= hi) continue;
+      const uint32_t s = index / v.cut.divisor;
+      const uint32_t col = seg.head[s] + (index - s * v.cut.divisor) * K;
+      Vec<DT> x;
+      x.set(dev::ld_global_v4(seg.at<DT>(s, col)));
+#pragma unroll
+      for (int j = 0; j < K; ++j)
+        if (x.get(j) >= threshold) offer(t, x.get(j), s * v.shard + col + j);
+    }
+  }
+  __syncthreads();
+  const int n = t.candidates;
+  if (t.works <= kMaxWork && n <= kMaxCandidates) sort_candidates(t, n, k);
+  else select_by_scan<DT>(v, seg, lo, hi, edges, t, k);
+}
+
+struct ClusterTop {
+  uint64_t list[kForwardCluster][kMaxTop];
+  uint64_t count[kForwardCluster];
+  int place[kMaxTop];
+};
+
+template <int DT, bool TOP>
+__global__ void __launch_bounds__(kThreads) log_probs_kernel(const __grid_constant__ LogProbsArgs a) {
+  extern __shared__ __align__(16) unsigned char dynamic[];
+  __shared__ Segments seg;
+  __shared__ JoinSlots slots;
+  TopSlots* top = reinterpret_cast<TopSlots*>(dynamic);
+  ClusterTop* both = reinterpret_cast<ClusterTop*>(dynamic + sizeof(TopSlots));
+  const VocabArgs& v = a.v;
+  const uint32_t ctas = cluster_size(), cta = cluster_rank();
+  uint16_t* tops = reinterpret_cast<uint16_t*>(dynamic + sizeof(TopSlots) + (ctas > 1 ? sizeof(ClusterTop) : 0));
+  const uint32_t per = (v.cut.vectors + ctas - 1) / ctas;
+  const uint32_t lo = min(v.cut.vectors, cta * per), hi = min(v.cut.vectors, lo + per);
+  start(ctas);
+  if (threadIdx.x == 0) dev::record_sm(v.sm_mask);
+  int phase = 0;
+  for (uint64_t t = blockIdx.x / ctas; t < v.rows; t += gridDim.x / ctas) {
+    const int64_t token = a.tokens ? a.tokens[t] : 0;
+    const bool scored = token >= 0 && token < v.vocab;  // the same in every thread of the cluster
+    Stats st{0.f, 0.f, 0.f};
+    float x = 0.f, thread_max = 0.f;
+    if (scored) {
+      __syncthreads();  // the last row's segments are done with
+      set_segments<DT>(v, t, seg);
+      __syncthreads();
+      if (a.tokens && threadIdx.x == 0)
+        x = load_one<DT>(seg.at_column<DT>(v, static_cast<uint32_t>(token)));
+      st = row_stats<DT, TOP>(v, seg, lo, hi, cta, ctas, slots, phase, tops, a.batch_shift, thread_max);
+    }
+    if (threadIdx.x == 0 && cta == 0) {
+      if (a.tokens) a.log_probs[t] = scored ? st.log_prob(x, v.inv_temp) : 0.f;
+      if (a.entropy) a.entropy[t] = st.entropy;
+      if (a.stats) {
+        a.stats[2 * t] = st.max;
+        a.stats[2 * t + 1] = st.log2_s * kLn2;
+      }
+    }
+    if (!TOP) continue;
+    const int k = a.top_k;
+    float* out_lp = a.top_log_probs + t * k;
+    int64_t* out_id = a.top_ids + t * k;
+    int found = 0;
+    if (scored && !st.bad()) {
+      select_top<DT>(v, seg, lo, hi, cta == 0, *top, k, tops, a.batch_shift, thread_max,
+                     !(fabsf(st.max) < -kClamp));
+      const int mine = top->found;
+      if (ctas == 1) {
+        found = mine;
+        for (int i = threadIdx.x; i < mine; i += kThreads) {
+          out_lp[i] = st.log_prob(key_value(top->sorted[i]), v.inv_temp);
+          out_id[i] = key_column(top->sorted[i]);
+        }
+      } else {
+        // every CTA gets every CTA's sorted list and places its own keys by
+        // the number of larger ones in each list
+        for (int i = threadIdx.x; i < mine * static_cast<int>(ctas); i += kThreads)
+          remote_store(remote(&both->list[cta][i / ctas], i % ctas), top->sorted[i / ctas]);
+        if (threadIdx.x < ctas) remote_store(remote(&both->count[cta], threadIdx.x), static_cast<uint64_t>(mine));
+        if (threadIdx.x < k) both->place[threadIdx.x] = 0;
+        cluster_barrier();
+        for (int i = threadIdx.x; i < mine * static_cast<int>(ctas); i += kThreads) {
+          const uint64_t key = top->sorted[i / ctas];
+          const uint64_t* list = both->list[i % ctas];
+          int l = 0, h = static_cast<int>(both->count[i % ctas]);
+          while (l < h) {
+            const int mid = (l + h) / 2;
+            if (list[mid] > key) l = mid + 1;
+            else h = mid;
+          }
+          if (l) atomicAdd(&both->place[i / ctas], l);
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < mine; i += kThreads) {
+          const int place = both->place[i];
+          if (place >= k) continue;
+          out_lp[place] = st.log_prob(key_value(top->sorted[i]), v.inv_temp);
+          out_id[place] = key_column(top->sorted[i]);
+        }
+        for (uint32_t q = 0; q < ctas; ++q) found += static_cast<int>(both->count[q]);
+      }
+    }
+    if (cta == 0)
+      for (int i = found + threadIdx.x; i < k; i += kThreads) {
+        out_lp[i] = scored && st.bad() ? NAN : -INFINITY;
+        out_id[i] = -1;
+      }
+  }
+}
+
+// ---------------------------------------------------------------- distillation
+template <int DT>
+__global__ void __launch_bounds__(kThreads) distill_kernel(const __grid_constant__ DistillArgs a) {
+  __shared__ Segments seg;
+  __shared__ JoinSlots slots;
+  __shared__ LossSlots loss;
+  const VocabArgs& v = a.v;
+  const uint32_t ctas = cluster_size(), cta = cluster_rank();
+  const uint32_t per = (v.cut.vectors + ctas - 1) / ctas;
+  const uint32_t lo = min(v.cut.vectors, cta * per), hi = min(v.cut.vectors, lo + per);
+  start(ctas);
+  if (threadIdx.x == 0) dev::record_sm(v.sm_mask);
+  int phase = 0;
+  for (uint64_t t = blockIdx.x / ctas; t < v.rows; t += gridDim.x / ctas) {
+    __syncthreads();  // the last row's segments are done with
+    set_segments<DT>(v, t, seg);
+    __syncthreads();
+    const bool mine = cta == 0 && threadIdx.x < 32;
+    if (mine) set_loss<DT>(v, seg, read_teacher(a, t), loss);
+    float unused;
+    const Stats st = row_stats<DT, false>(v, seg, lo, hi, cta, ctas, slots, phase, nullptr, 0, unused);
+    if (mine) store_loss(a, t, loss, st);
+  }
+}
+
+// CTAs of one row: as many as keep every SM at no more than four, but none
+// whose slice is less than one batch of every thread.
+int cluster_for(const VocabArgs& v, const VocabLaunch& l) {
+  int c = 1;
+  while (c < kForwardCluster && v.rows * c * 2 <= static_cast<uint64_t>(l.sm_count) * 4 &&
+         v.cut.vectors >= static_cast<uint32_t>(2 * c * kThreads * kBatch) && (l.cap <= 0 || 2 * c <= l.cap))
+    c *= 2;
+  return c;
+}
+
+uint64_t grid_for(const VocabArgs& v, const VocabLaunch& l, int cluster) {
+  uint64_t rows = v.rows;
+  if (l.cap > 0 && rows * cluster > static_cast<uint64_t>(l.cap)) rows = l.cap / cluster;
+  // far more rows than fit at once: a bounded grid takes the rest in turn
+  const uint64_t most = static_cast<uint64_t>(1) << 20;
+  return (rows < most ? rows : most) * cluster;
+}
+
+template <int DT, bool TOP>
+int launch_log_probs_t(LogProbsArgs& a, VocabLaunch& l) {
+  set_cut<DT>(a.v, kThreads, 0);
+  const int c = cluster_for(a.v, l);
+  size_t smem = 0;
+  a.batches = a.batch_shift = 0;
+  if (TOP) {
+    const uint32_t per = (a.v.cut.vectors + c - 1) / c;
+    a.batches = static_cast<int>((per + kThreads * kBatch - 1) / (kThreads * kBatch));
+    while (((a.batches + (1 << a.batch_shift) - 1) >> a.batch_shift) > kMaxEntries) ++a.batch_shift;
+    const int entries = (a.batches + (1 << a.batch_shift) - 1) >> a.batch_shift;
+    smem = sizeof(TopSlots) + (c > 1 ? sizeof(ClusterTop) : 0) + sizeof(uint16_t) * kThreads * entries;
+    const cudaError_t e = cudaFuncSetAttribute(log_probs_kernel<DT, TOP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(smem));
+    if (e != cudaSuccess) return static_cast<int>(e);
+  }
+  return launch_rows(log_probs_kernel<DT, TOP>, a, l, grid_for(a.v, l, c), kThreads, c, smem);
+}
+
+template <int DT>
+int launch_distill_t(DistillArgs& a, VocabLaunch& l) {
+  set_cut<DT>(a.v, kThreads, 0);
+  const int c = cluster_for(a.v, l);
+  return launch_rows(distill_kernel<DT>, a, l, grid_for(a.v, l, c), kThreads, c, 0);
+}
+
+}  // namespace
+
+int launch_log_probs(int dtype, LogProbsArgs& a, VocabLaunch& l) {
+  if (dtype == kBF16) return a.top_k ? launch_log_probs_t<kBF16, true>(a, l) : launch_log_probs_t<kBF16, false>(a, l);
+  return a.top_k ? launch_log_probs_t<kF32, true>(a, l) : launch_log_probs_t<kF32, false>(a, l);
+}
+
+namespace vocab {
+int launch_distill_forward(int dtype, DistillArgs& a, VocabLaunch& l) {
+  return dtype == kBF16 ? launch_distill_t<kBF16>(a, l) : launch_distill_t<kF32>(a, l);
+}
+}  // namespace vocab
+
+}  // namespace tccl

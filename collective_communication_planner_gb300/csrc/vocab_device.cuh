@@ -1,0 +1,558 @@
+// Device code shared by the vocabulary-parallel operators' kernels: how a row
+// is walked over the rank buffers, and its softmax statistics.
+#pragma once
+
+#include <cfloat>
+#include <cmath>
+
+#include "dispatch.cuh"
+#include "vocab.h"
+
+namespace tccl {
+namespace vocab {
+
+constexpr float kLn2 = 0.69314718056f;
+constexpr float kLog2e = 1.44269504089f;
+// Logits are clamped here before the fast arithmetic, so that masked places
+// (-inf or the type's lowest value) have a finite distance from the maximum
+// and 0 * distance is 0. A row whose maximum is not within (-2^100, 2^100) is
+// worked out again by slow_stats.
+constexpr float kClamp = -0x1p100f;
+
+template <int DT> struct Elem;
+template <> struct Elem<kBF16> {
+  static constexpr int kVec = 8;   // elements of a 16-byte vector
+  static constexpr int kBytes = 2;
+};
+template <> struct Elem<kF32> {
+  static constexpr int kVec = 4;
+  static constexpr int kBytes = 4;
+};
+
+// ---------------------------------------------------------------- arithmetic
+// 2^d; results below 2^-126 are 0
+__device__ __forceinline__ float exp2_ftz(float d) {
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(d));
+  return e;
+}
+
+// two fp32 numbers in one register pair, for the packed pipe
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pack(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack(f32x2 v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 exp2x2(f32x2 d) {
+  float lo, hi;
+  unpack(d, lo, hi);
+  return pack(exp2_ftz(lo), exp2_ftz(hi));
+}
+
+// maxima that keep NaN
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ float max_f32(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+template <int DT>
+__device__ __forceinline__ float load_one(const char* p) {
+  if (DT == kBF16) return __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(p));
+  return *reinterpret_cast<const float*>(p);
+}
+
+template <int DT>
+__device__ __forceinline__ void store_one(char* p, float x) {
+  if (DT == kBF16) *reinterpret_cast<__nv_bfloat16*>(p) = __float2bfloat16_rn(x);
+  else *reinterpret_cast<float*>(p) = x;
+}
+
+// A 16-byte vector of logits.
+template <int DT>
+struct Vec {
+  static constexpr int kPairs = Elem<DT>::kVec / 2;
+  uint32_t w[4];
+
+  __device__ __forceinline__ void set(uint4 x) {
+    w[0] = x.x;
+    w[1] = x.y;
+    w[2] = x.z;
+    w[3] = x.w;
+  }
+  // a vector of clamped places: adds nothing to a row's sums
+  __device__ __forceinline__ void set_empty() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = DT == kBF16 ? 0xF180F180u : 0xF1800000u;
+  }
+  __device__ __forceinline__ void clamp() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = DT == kBF16 ? max_bf16x2(w[i], 0xF180F180u)
+                         : __float_as_uint(max_f32(__uint_as_float(w[i]), kClamp));
+  }
+  __device__ __forceinline__ f32x2 pair(int i) const {
+    if (DT == kBF16) return pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+    return pack(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+  }
+  __device__ __forceinline__ float get(int i) const {
+    if (DT == kBF16) return __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+    return __uint_as_float(w[i]);
+  }
+  __device__ __forceinline__ void put_pair(int i, f32x2 v) {
+    float lo, hi;
+    unpack(v, lo, hi);
+    if (DT == kBF16) {
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(hi), "f"(lo));
+    } else {
+      w[2 * i] = __float_as_uint(lo);
+      w[2 * i + 1] = __float_as_uint(hi);
+    }
+  }
+  __device__ __forceinline__ uint4 out() const { return make_uint4(w[0], w[1], w[2], w[3]); }
+};
+
+template <int DT, int N>
+__device__ __forceinline__ float batch_max(const Vec<DT> (&x)[N]) {
+  if (DT == kBF16) {
+    uint32_t m = x[0].w[0];
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m = max_bf16x2(m, x[k].w[i]);
+    return max_f32(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+  }
+  float m = __uint_as_float(x[0].w[0]);
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = max_f32(m, __uint_as_float(x[k].w[i]));
+  return m;
+}
+
+// ---------------------------------------------------------------- statistics
+// Part of a row's softmax: the maximum m, s = sum 2^(x c - r) and
+// u = sum 2^(x c - r) (x c - r) with c = log2(e) / temperature and the
+// reference r = m c rounded to fp32. x c - r is one fused operation, so it is
+// exact but for one rounding however far the logits are from zero.
+struct Part {
+  float m, s, u;
+};
+
+__device__ __forceinline__ void rebase(Part& a, float m, float c) {
+  if (a.m == m) return;
+  const float d = __fsub_rn(__fmul_rn(a.m, c), __fmul_rn(m, c));
+  const float f = exp2_ftz(d);
+  a.u = f == 0.f ? 0.f : f * (a.u + a.s * d);
+  a.s *= f;
+  a.m = m;
+}
+
+// the first `n` (a power of two) lanes' parts joined, the same bits in each of them
+template <int N>
+__device__ __forceinline__ Part lanes_join(Part a, float c) {
+  float m = a.m;
+#pragma unroll
+  for (int o = N / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  rebase(a, m, c);
+#pragma unroll
+  for (int o = N / 2; o > 0; o >>= 1) {
+    a.s += __shfl_xor_sync(0xFFFFFFFFu, a.s, o);
+    a.u += __shfl_xor_sync(0xFFFFFFFFu, a.u, o);
+  }
+  return a;
+}
+
+constexpr int kMaxWarps = 32;
+constexpr int kMaxCluster = 16;
+
+struct JoinSlots {
+  Part warp[2][kMaxWarps];
+  Part cta[2][kMaxCluster];
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+// every thread of the cluster; orders shared-memory writes, remote ones too
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// the shared::cluster address of `p` in CTA `rank`
+__device__ __forceinline__ uint32_t remote(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(dev::smem_addr(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void remote_store(uint32_t at, float x) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(x) : "memory");
+}
+__device__ __forceinline__ void remote_store(uint32_t at, uint64_t x) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(x) : "memory");
+}
+
+// Joins the parts of all threads of the cluster; every thread gets the result,
+// the same bits. Slots alternate between two sets: a set is written again two
+// joins later, past a barrier that every reader of it has reached.
+__device__ __forceinline__ Part row_join(Part a, float c, JoinSlots& slots, int& phase, uint32_t csize) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  a = lanes_join<32>(a, c);
+  if (lane == 0) slots.warp[phase][warp] = a;
+  __syncthreads();
+  const Part none{kClamp, 0.f, 0.f};
+  a = lanes_join<32>(lane < warps ? slots.warp[phase][lane] : none, c);
+  if (csize > 1) {
+    if (warp == 0 && lane < csize) {
+      const uint32_t at = remote(&slots.cta[phase][cluster_rank()], lane);
+      remote_store(at, a.m);
+      remote_store(at + 4, a.s);
+      remote_store(at + 8, a.u);
+    }
+    cluster_barrier();
+    a = lanes_join<32>(lane < csize ? slots.cta[phase][lane] : none, c);
+  }
+  phase ^= 1;
+  return a;
+}
+
+// A row's statistics: maximum, log2 of the sum relative to it, and the
+// entropy in natural units. log_s is NaN for a row that holds NaN or +inf.
+struct Stats {
+  float max, log2_s, entropy;
+  __device__ __forceinline__ bool empty() const { return max == -INFINITY; }
+  __device__ __forceinline__ bool bad() const { return log2_s != log2_s; }
+  // log probability of a logit
+  __device__ __forceinline__ float log_prob(float x, float inv_temp) const {
+    if (x == -INFINITY && !bad()) return x;
+    return (x - max) * inv_temp - log2_s * kLn2;
+  }
+};
+
+__device__ __forceinline__ Stats stats_of(const Part& a, float c) {
+  Stats r;
+  r.max = a.m;
+  const float l = log2f(a.s);
+  // the sum is relative to the rounded m c: move it to the exact product
+  r.log2_s = l - __fmaf_rn(a.m, c, -__fmul_rn(a.m, c));
+  r.entropy = kLn2 * (l - a.u / a.s);
+  return r;
+}
+
+// ---------------------------------------------------------------- row walk
+// The segments of the current row, one per used rank, in shared memory: the
+// first element, and how many elements come before the first whole vector.
+struct Segments {
+  const char* src[kMaxRanks];
+  uint32_t head[kMaxRanks];
+  template <int DT>
+  __device__ __forceinline__ const char* at(uint32_t seg, uint32_t col) const {
+    return src[seg] + static_cast<uint64_t>(col) * Elem<DT>::kBytes;
+  }
+  // element `column` of the whole row
+  template <int DT>
+  __device__ __forceinline__ const char* at_column(const VocabArgs& v, uint32_t column) const {
+    const uint32_t seg = column / v.shard;
+    return at<DT>(seg, column - seg * v.shard);
+  }
+};
+
+// thread r < used sets rank r's segment of row t; the caller synchronises
+template <int DT>
+__device__ __forceinline__ void set_segments(const VocabArgs& v, uint64_t t, Segments& s) {
+  if (threadIdx.x < v.used) {
+    const char* at = static_cast<const char*>(v.p.src[threadIdx.x]) + t * v.src_stride * Elem<DT>::kBytes;
+    s.src[threadIdx.x] = at;
+    s.head[threadIdx.x] = static_cast<uint32_t>(-reinterpret_cast<uintptr_t>(at) & 15) / Elem<DT>::kBytes;
+  }
+}
+
+// The vectors first, first + blockDim, ... of a row, in (segment, vector) form.
+struct Walk {
+  uint32_t index, seg, vec;
+  __device__ __forceinline__ Walk(const VocabCut& c, uint32_t first)
+      : index(first), seg(first / c.divisor), vec(first - seg * c.divisor) {}
+  __device__ __forceinline__ void next(const VocabCut& c) {
+    index += blockDim.x;
+    seg += c.step_seg;
+    vec += c.step_vec;
+    if (vec >= c.divisor) {
+      vec -= c.divisor;
+      ++seg;
+    }
+  }
+};
+
+// segment of edge element `e` of a row, and its column there
+template <int DT>
+__device__ __forceinline__ void edge_at(const VocabArgs& v, const Segments& s, uint32_t e, uint32_t& seg,
+                                        uint32_t& col) {
+  seg = v.used - 1;
+  uint32_t vectors = v.cut.last;
+  if (e < seg * v.cut.edge) {
+    seg = e / v.cut.edge;
+    vectors = v.cut.full;
+  }
+  col = e - seg * v.cut.edge;
+  if (col >= s.head[seg]) col += vectors * Elem<DT>::kVec;
+}
+
+// calls f(x, column) for this thread's elements of vectors [lo, hi) of the
+// row, one element at a time, and of its edges where `edges` is set
+template <int DT, typename F>
+__device__ void each_element(const VocabArgs& v, const Segments& s, uint32_t lo, uint32_t hi, bool edges, F f) {
+  constexpr uint32_t K = Elem<DT>::kVec;
+  for (Walk w(v.cut, lo + threadIdx.x); w.index < hi; w.next(v.cut)) {
+    const uint32_t col = s.head[w.seg] + w.vec * K;
+    for (uint32_t i = 0; i < K; ++i) f(load_one<DT>(s.at<DT>(w.seg, col + i)), w.seg * v.shard + col + i);
+  }
+  for (uint32_t e = threadIdx.x; edges && e < v.cut.edges; e += blockDim.x) {
+    uint32_t seg, col;
+    edge_at<DT>(v, s, e, seg, col);
+    f(load_one<DT>(s.at<DT>(seg, col)), seg * v.shard + col);
+  }
+}
+
+// The statistics of a row whose maximum is not within (-2^100, 2^100), where
+// the products of the fast arithmetic may overflow: the maximum first, then
+// the sums of 2^((x - max) c), the distance taken before the product.
+template <int DT>
+__device__ __noinline__ Stats slow_stats(const VocabArgs& v, const Segments& s, uint32_t lo, uint32_t hi,
+                                         JoinSlots& slots, int& phase, uint32_t cta, uint32_t ctas) {
+  float m = -INFINITY;
+  each_element<DT>(v, s, lo, hi, cta == 0, [&](float x, uint32_t) { m = fmaxf(m, x); });
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  // max and sum joined apart, in the slots of two joins
+  for (int round = 0; round < 2; ++round) {
+    float p = m, q = 0.f;  // round 0: the maximum; round 1: s and u
+    if (round == 1) {
+      p = 0.f;
+      each_element<DT>(v, s, lo, hi, cta == 0, [&](float x, uint32_t) {
+        if (x == -INFINITY) return;
+        const float d = (x - m) * v.exp2_scale, e = exp2_ftz(d);
+        p += e;
+        if (e != 0.f) q += e * d;
+      });
+    }
+    const auto join = [&](float& a, float b) { a = round == 0 ? fmaxf(a, b) : a + b; };
+    for (int stage = 0; stage < (ctas > 1 ? 3 : 2); ++stage) {
+      const float none = round == 0 ? -INFINITY : 0.f;
+      if (stage == 1) {
+        if (lane == 0) slots.warp[phase][warp] = Part{p, q, 0.f};
+        __syncthreads();
+        p = lane < warps ? slots.warp[phase][lane].m : none;
+        q = lane < warps ? slots.warp[phase][lane].s : 0.f;
+      } else if (stage == 2) {
+        if (warp == 0 && lane < ctas) {
+          const uint32_t at = remote(&slots.cta[phase][cta], lane);
+          remote_store(at, p);
+          remote_store(at + 4, q);
+        }
+        cluster_barrier();
+        p = lane < ctas ? slots.cta[phase][lane].m : none;
+        q = lane < ctas ? slots.cta[phase][lane].s : 0.f;
+      }
+      for (int o = 16; o > 0; o >>= 1) {
+        join(p, __shfl_xor_sync(0xFFFFFFFFu, p, o));
+        q += __shfl_xor_sync(0xFFFFFFFFu, q, o);
+      }
+    }
+    phase ^= 1;
+    if (round == 0) {
+      m = p;
+    } else {
+      Stats r;
+      r.max = m;
+      r.log2_s = m == -INFINITY && !(p != p) ? 0.f : log2f(p);
+      r.entropy = m == -INFINITY && !(p != p) ? 0.f : kLn2 * (r.log2_s - q / p);
+      return r;
+    }
+  }
+  return Stats{};
+}
+
+// ---------------------------------------------------------------- teacher
+// A teacher's entries of one row in the lanes of a warp, entry 32 i + lane in
+// slot i: column (-1: empty), q and log q; total = sum q in every lane.
+struct TeacherRow {
+  int32_t column[kMaxTop / 32];
+  float q[kMaxTop / 32], log_q[kMaxTop / 32];
+  float total;
+};
+
+__device__ __forceinline__ TeacherRow read_teacher(const DistillArgs& a, uint64_t t) {
+  constexpr int N = kMaxTop / 32;
+  const int lane = threadIdx.x & 31;
+  TeacherRow r;
+  float top = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int k = 32 * i + lane;
+    r.column[i] = -1;
+    r.log_q[i] = -INFINITY;
+    if (k < a.top_k) {
+      const uint64_t o = t * a.top_k + k;
+      const int64_t id = a.ids[o];
+      if (id >= 0 && id < a.v.vocab) {
+        r.column[i] = static_cast<int32_t>(id);
+        const float x = a.teacher_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.teacher)[o])
+                                       : static_cast<const float*>(a.teacher)[o];
+        r.log_q[i] = x * a.v.inv_temp;
+      }
+    }
+    top = fmaxf(top, r.log_q[i]);
+  }
+  float lse;
+  if (a.teacher_lse) {
+    lse = a.teacher_lse[t];
+  } else {
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    if (top == -INFINITY) top = 0.f;
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) sum += expf(r.log_q[i] - top);
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    lse = sum == 0.f ? 0.f : top + logf(sum);
+  }
+  r.total = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    r.log_q[i] -= lse;
+    r.q[i] = expf(r.log_q[i]);
+    r.total += r.q[i];
+  }
+  for (int o = 16; o > 0; o >>= 1) r.total += __shfl_xor_sync(0xFFFFFFFFu, r.total, o);
+  return r;
+}
+
+// What the loss needs of the entries, in shared memory: warp 0 writes it, with
+// the student's logits at the entries' columns, and reads it after the row's join.
+struct LossSlots {
+  float q[kMaxTop], log_q[kMaxTop], x[kMaxTop];
+};
+
+template <int DT>
+__device__ __forceinline__ void set_loss(const VocabArgs& v, const Segments& s, const TeacherRow& r, LossSlots& l) {
+#pragma unroll
+  for (int i = 0; i < kMaxTop / 32; ++i) {
+    const int k = 32 * i + (threadIdx.x & 31);
+    l.q[k] = r.q[i];
+    l.log_q[k] = r.log_q[i];
+    l.x[k] = r.column[i] >= 0 ? load_one<DT>(s.at_column<DT>(v, r.column[i])) : 0.f;
+  }
+}
+
+// Warp 0: writes sum_k q_k (log q_k - log p_k) and the statistics of row t.
+__device__ __forceinline__ void store_loss(const DistillArgs& a, uint64_t t, const LossSlots& l, const Stats& st) {
+  float loss = 0.f;
+#pragma unroll
+  for (int i = 0; i < kMaxTop / 32; ++i) {
+    const int k = 32 * i + (threadIdx.x & 31);
+    if (!(l.q[k] <= 0.f)) loss += l.q[k] * (l.log_q[k] - st.log_prob(l.x[k], a.v.inv_temp));
+  }
+  for (int o = 16; o > 0; o >>= 1) loss += __shfl_xor_sync(0xFFFFFFFFu, loss, o);
+  if ((threadIdx.x & 31) == 0) {
+    a.loss[t] = loss;
+    if (a.stats) {
+      a.stats[2 * t] = st.max;
+      a.stats[2 * t + 1] = st.log2_s * kLn2;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- host side
+// Cuts a row into vectors and edges. `spare`: vectors of a segment given up to
+// the edges at the most, where rows do not start on 16-byte boundaries.
+template <int DT>
+inline void set_cut(VocabArgs& v, int threads, int spare) {
+  constexpr uint32_t K = Elem<DT>::kVec;
+  const uint32_t last = v.vocab - (v.used - 1) * v.shard;
+  const auto vectors = [&](uint32_t n) {
+    const uint32_t lost = v.aligned ? 0 : K - 1 + spare * K;
+    return n < lost ? 0u : (n - lost) / K;
+  };
+  VocabCut& c = v.cut;
+  c.full = vectors(v.shard);
+  c.last = vectors(last);
+  c.divisor = c.full > 0 ? c.full : 1;
+  c.vectors = (v.used - 1) * c.full + c.last;
+  c.edge = v.shard - c.full * K;
+  c.edges = (v.used - 1) * c.edge + last - c.last * K;
+  c.step_seg = threads / c.divisor;
+  c.step_vec = threads % c.divisor;
+}
+
+int launch_distill_forward(int dtype, DistillArgs& a, VocabLaunch& l);
+
+// Launches `kernel` on clusters of `cluster` CTAs; uncapped calls start early
+// (the kernel waits before it touches memory).
+template <typename Kernel, typename Args>
+inline int launch_rows(Kernel kernel, const Args& a, VocabLaunch& l, uint64_t grid, int threads, int cluster,
+                       size_t smem) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = static_cast<cudaStream_t>(l.stream);
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  if (l.cap <= 0) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (cluster > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[n].val.clusterDim.y = 1;
+    attr[n++].val.clusterDim.z = 1;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
+  l.ctas = static_cast<int>(grid);
+  l.threads = threads;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
+  if (e != cudaSuccess) return static_cast<int>(e);
+  return static_cast<int>(cudaGetLastError());
+}
+
+// The start of every kernel: the cluster's CTAs meet before any of them writes
+// to another's shared memory, and the previous kernel of the stream ends
+// before any global access.
+__device__ __forceinline__ void start(uint32_t ctas) {
+  if (ctas > 1) cluster_barrier();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+}  // namespace vocab
+}  // namespace tccl

@@ -1,6 +1,7 @@
 // C entry points of the operators over vocabulary-parallel logits
 // (include/tccl.h): argument validation and launches. Host code only; the
-// kernels are in kernels_vocab.cu.
+// kernels are in kernels_vocab_forward.cu and
+// kernels_vocab_grad.cu.
 #include "vocab.h"
 
 #include <cuda_runtime.h>
@@ -98,6 +99,13 @@ bool fill(tcclGroup* g, const void* const* logits, const tcclVocab_t* shape, voi
     dst[r] = Block{(uintptr_t)grads[r], shape->rows, shape->shard * es, grad_stride * es};
     v->p.dst[r] = grads[r];
   }
+  // 16-byte accesses from the first element of every row on
+  const auto whole = [&](size_t stride, void* const* p) {
+    bool ok = stride * es % 16 == 0 || shape->rows == 1;
+    for (int r = 0; r < g->nranks; ++r) ok = ok && (uintptr_t)p[r] % 16 == 0;
+    return ok;
+  };
+  v->aligned = whole(shape->row_stride, const_cast<void* const*>(logits)) && (!grads || whole(grad_stride, grads));
   v->rows = shape->rows;
   v->src_stride = shape->row_stride;
   v->dst_stride = grad_stride;
@@ -112,14 +120,17 @@ bool fill(tcclGroup* g, const void* const* logits, const tcclVocab_t* shape, voi
 
 // Launches on the group's device and notes the launch shape.
 template <typename Args>
-tcclResult_t run(tcclGroup* g, int (*launch)(int, const Args&, int, int, int*, int*, void*), Args& a,
-                 int dtype, int cap, cudaStream_t stream) {
+tcclResult_t run(tcclGroup* g, int (*launch)(int, Args&, VocabLaunch&), Args& a, int dtype, int cap,
+                 cudaStream_t stream) {
   int cur = -1;
   if (cudaGetDevice(&cur) != cudaSuccess) return tcclCudaError;
   if (cur != g->device && cudaSetDevice(g->device) != cudaSuccess) return tcclCudaError;
   a.v.sm_mask = sm_record_slot(g);
   std::memset(&g->last, 0, sizeof(g->last));
-  const int err = launch(dtype, a, g->dev.sm_count, cap, &g->last.ctas, &g->last.threads, stream);
+  VocabLaunch l{g->dev.sm_count, cap, stream, 0, 0};
+  const int err = launch(dtype, a, l);
+  g->last.ctas = l.ctas;
+  g->last.threads = l.threads;
   if (cur != g->device) cudaSetDevice(cur);
   return err == 0 ? tcclSuccess : tcclCudaError;
 }
