@@ -8,42 +8,10 @@ namespace {
 using namespace vocab;
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 4;          // vectors a thread loads together
-constexpr int kMaxEntries = 64;    // stored batch maxima per thread
-constexpr int kMaxWork = 512;      // batches looked at again for alternatives
+constexpr int kMaxEntries = 64;    // stored chunk maxima per thread
+constexpr int kMaxWork = 512;      // of them looked at again for alternatives
 constexpr int kMaxCandidates = 1024;
 constexpr int kForwardCluster = 8;
-
-// Adds a batch to a thread's part: the largest element first, then the sums.
-template <int DT>
-__device__ __forceinline__ float add_batch(Part& a, float& r, f32x2 (&s)[2], f32x2 (&u)[2], Vec<DT> (&x)[kBatch], float c) {
-#pragma unroll
-  for (int k = 0; k < kBatch; ++k) x[k].clamp();
-  const float top = batch_max<DT, kBatch>(x);
-  if (top > a.m) {
-    const float to = __fmul_rn(top, c), d = __fsub_rn(r, to), f = exp2_ftz(d);
-    const f32x2 dd = pack(d, d), ff = pack(f, f);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      // d may be -inf only where f is 0 and s is 0 or vanishes
-      u[i] = f == 0.f ? 0ull : mul2(ff, fma2(s[i], dd, u[i]));
-      s[i] = f == 0.f ? 0ull : mul2(ff, s[i]);
-    }
-    a.m = top;
-    r = to;
-  }
-  const f32x2 cc = pack(c, c), rr = pack(-r, -r);
-#pragma unroll
-  for (int k = 0; k < kBatch; ++k)
-#pragma unroll
-    for (int i = 0; i < Vec<DT>::kPairs; ++i) {
-      const f32x2 d = fma2(x[k].pair(i), cc, rr);
-      const f32x2 e = exp2x2(d);
-      s[i & 1] = add2(s[i & 1], e);
-      u[i & 1] = fma2(e, d, u[i & 1]);
-    }
-  return top;
-}
 
 // The smallest bf16 number that is not below x, as its bits.
 __device__ __forceinline__ uint16_t bf16_above(float x) {
@@ -51,60 +19,20 @@ __device__ __forceinline__ uint16_t bf16_above(float x) {
   return static_cast<uint16_t>((b & 0x80000000u) ? b >> 16 : (b + 0xFFFFu) >> 16);
 }
 
-// This thread's part of vectors [lo, hi) of the row, and of its edge elements
-// where `edges` is set.
-// With TOP, the maximum of every 2^shift batches is kept in `tops`, for the
-// alternatives.
-template <int DT, bool TOP>
-__device__ __forceinline__ Part scan_row(const VocabArgs& v, const Segments& seg, uint32_t lo, uint32_t hi,
-                                         bool edges, uint16_t* tops, int shift) {
-  const float c = v.exp2_scale;
-  Part a{kClamp, 0.f, 0.f};
-  float r = __fmul_rn(kClamp, c);
-  f32x2 s[2] = {0, 0}, u[2] = {0, 0};
-  int batch = 0;
-  float entry = kClamp;
-  for (Walk w(v.cut, lo + threadIdx.x); w.index < hi;) {
-    Vec<DT> x[kBatch];
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      if (w.index < hi) x[k].set(dev::ld_global_v4(seg.at<DT>(w.seg, seg.head[w.seg] + w.vec * Elem<DT>::kVec)));
-      else x[k].set_empty();
-      w.next(v.cut);
-    }
-    const float top = add_batch<DT>(a, r, s, u, x, c);
-    if (TOP) {
-      entry = fmaxf(entry, top);
-      if ((++batch & ((1 << shift) - 1)) == 0 || w.index >= hi) {
-        tops[((batch - 1) >> shift) * kThreads + threadIdx.x] = bf16_above(entry);
-        entry = kClamp;
-      }
-    }
-  }
-  float s0, s1, s2, s3;
-  unpack(s[0], s0, s1);
-  unpack(s[1], s2, s3);
-  a.s = (s0 + s1) + (s2 + s3);
-  unpack(u[0], s0, s1);
-  unpack(u[1], s2, s3);
-  a.u = (s0 + s1) + (s2 + s3);
-  for (uint32_t e = threadIdx.x; edges && e < v.cut.edges; e += kThreads) {
-    uint32_t es, col;
-    edge_at<DT>(v, seg, e, es, col);
-    const float x = max_f32(load_one<DT>(seg.at<DT>(es, col)), kClamp);
-    if (x > a.m) rebase(a, x, c);
-    const float d = __fmaf_rn(x, c, -__fmul_rn(a.m, c)), p = exp2_ftz(d);
-    a.s += p;
-    a.u = __fmaf_rn(p, d, a.u);
-  }
-  return a;
-}
-
-template <int DT, bool TOP>
+// The statistics of a row over the cluster. With TOP, the maximum of every
+// 2^shift chunks is kept in `tops` for the alternatives, and thread_max set.
+template <int DT, bool ENTROPY, bool TOP>
 __device__ __forceinline__ Stats row_stats(const VocabArgs& v, const Segments& seg, uint32_t lo, uint32_t hi,
                                            uint32_t cta, uint32_t ctas, JoinSlots& slots, int& phase,
                                            uint16_t* tops, int shift, float& thread_max) {
-  Part a = scan_row<DT, TOP>(v, seg, lo, hi, cta == 0, tops, shift);
+  int chunk = 0;
+  float entry = kClamp;
+  Part a = scan_row<DT, ENTROPY, false>(v, seg, lo, hi, cta == 0, StreamLoad(), [&](float top) {
+    if (!TOP) return;
+    entry = fmaxf(entry, top);
+    tops[(chunk >> shift) * kThreads + threadIdx.x] = bf16_above(entry);
+    if ((++chunk & ((1 << shift) - 1)) == 0) entry = kClamp;
+  });
   thread_max = a.m;
   a = row_join(a, v.exp2_scale, slots, phase, ctas);
   if (fabsf(a.m) < -kClamp) return stats_of(a, v.exp2_scale);
@@ -189,13 +117,14 @@ __device__ __noinline__ void select_by_scan(const VocabArgs& v, const Segments& 
     prune(false);
   };
   __syncthreads();
-  const uint32_t steps = (hi - lo + kThreads - 1) / kThreads;
-  Walk w(v.cut, lo + threadIdx.x);
-  for (uint32_t i = 0; i < steps; ++i, w.next(v.cut)) {
-    const bool on = w.index < hi;
-    const uint32_t col = on ? seg.head[w.seg] + w.vec * K : 0;
-    for (int j = 0; j < K; ++j)
-      take(on, on ? load_one<DT>(seg.at<DT>(w.seg, col + j)) : 0.f, w.seg * v.shard + col + j);
+  ChunkWalk w(v.cut, lo + threadIdx.x / 32);
+  for (uint32_t i = lo; i < hi; i += kThreads / 32, w.next(v.cut)) {
+    for (int k = 0; k < kBatch; ++k) {
+      const bool on = w.index < hi && w.vector() + k * 32 < w.vectors(v);
+      const uint32_t col = on ? seg.head[w.seg] + (w.vector() + k * 32) * K : 0;
+      for (int j = 0; j < K; ++j)
+        take(on, on ? load_one<DT>(seg.at<DT>(w.seg, col + j)) : 0.f, w.seg * v.shard + col + j);
+    }
   }
   for (uint32_t e0 = 0; edges && e0 < v.cut.edges; e0 += kThreads) {
     const uint32_t e = e0 + threadIdx.x;
@@ -207,10 +136,10 @@ __device__ __noinline__ void select_by_scan(const VocabArgs& v, const Segments& 
   prune(true);
 }
 
-// The best k columns among this CTA's vectors [lo, hi) and edge elements,
+// The best k columns among this CTA's chunks [lo, hi) and edge elements,
 // sorted, in t.sorted[0 .. t.found). The k-th largest of the threads' maxima
-// is at most the k-th largest element, so only batches whose maximum reaches
-// it are read again.
+// is at most the k-th largest element, so only chunks whose maximum reaches
+// it are read again, by the lanes.
 template <int DT>
 __device__ void select_top(const VocabArgs& v, const Segments& seg, uint32_t lo, uint32_t hi, bool edges,
                            TopSlots& t, int k, const uint16_t* tops, int shift,
@@ -237,8 +166,9 @@ __device__ void select_top(const VocabArgs& v, const Segments& seg, uint32_t lo,
   __syncthreads();
   // at the clamp: too few threads have an element above it, any element counts
   const float threshold = t.threshold > kClamp ? t.threshold : -INFINITY;
-  const int entries = lo + threadIdx.x < hi
-      ? (((hi - lo - threadIdx.x + kThreads - 1) / kThreads + kBatch - 1) / kBatch + (1 << shift) - 1) >> shift : 0;
+  const int warps = kThreads / 32, warp = threadIdx.x / 32;
+  const int chunks = lo + warp < hi ? (hi - lo - warp + warps - 1) / warps : 0;
+  const int entries = (chunks + (1 << shift) - 1) >> shift;
   for (int i = 0; i < entries; ++i) {
     if (__uint_as_float(static_cast<uint32_t>(tops[i * kThreads + threadIdx.x]) << 16) >= threshold) {
       const int n = atomicAdd(&t.works, 1);
@@ -255,16 +185,18 @@ __device__ void select_top(const VocabArgs& v, const Segments& seg, uint32_t lo,
   if (t.works <= kMaxWork) {
     const int per = kBatch << shift, items = t.works * per;
     for (int i = threadIdx.x; i < items; i += kThreads) {
-      const uint32_t job = t.work[i / per];
-      const uint32_t index = lo + (job / kThreads * per + i % per) * kThreads + job % kThreads;
-      if (index >= hi) continue;
-      const uint32_t s = index / v.cut.divisor;
-      const uint32_t col = seg.head[s] + (index - s * v.cut.divisor) * K;
+      const uint32_t job = t.work[i / per], thread = job % kThreads;
+      const uint32_t chunk = lo + ((job / kThreads << shift) + i % per / kBatch) * warps + thread / 32;
+      if (chunk >= hi) continue;
+      const ChunkWalk w(v.cut, chunk);
+      const uint32_t vec = w.part * kChunkVectors + i % kBatch * 32 + thread % 32;
+      if (vec >= w.vectors(v)) continue;
+      const uint32_t col = seg.head[w.seg] + vec * K;
       Vec<DT> x;
-      x.set(dev::ld_global_v4(seg.at<DT>(s, col)));
+      x.set(dev::ld_global_v4(seg.at<DT>(w.seg, col)));
 #pragma unroll
       for (int j = 0; j < K; ++j)
-        if (x.get(j) >= threshold) offer(t, x.get(j), s * v.shard + col + j);
+        if (x.get(j) >= threshold) offer(t, x.get(j), w.seg * v.shard + col + j);
     }
   }
   __syncthreads();
@@ -280,7 +212,7 @@ struct ClusterTop {
 };
 
 template <int DT, bool TOP>
-__global__ void __launch_bounds__(kThreads) log_probs_kernel(const __grid_constant__ LogProbsArgs a) {
+__global__ void __launch_bounds__(kThreads, 5) log_probs_kernel(const __grid_constant__ LogProbsArgs a) {
   extern __shared__ __align__(16) unsigned char dynamic[];
   __shared__ Segments seg;
   __shared__ JoinSlots slots;
@@ -289,8 +221,8 @@ __global__ void __launch_bounds__(kThreads) log_probs_kernel(const __grid_consta
   const VocabArgs& v = a.v;
   const uint32_t ctas = cluster_size(), cta = cluster_rank();
   uint16_t* tops = reinterpret_cast<uint16_t*>(dynamic + sizeof(TopSlots) + (ctas > 1 ? sizeof(ClusterTop) : 0));
-  const uint32_t per = (v.cut.vectors + ctas - 1) / ctas;
-  const uint32_t lo = min(v.cut.vectors, cta * per), hi = min(v.cut.vectors, lo + per);
+  const uint32_t per = (v.cut.chunks + ctas - 1) / ctas;
+  const uint32_t lo = min(v.cut.chunks, cta * per), hi = min(v.cut.chunks, lo + per);
   start(ctas);
   if (threadIdx.x == 0) dev::record_sm(v.sm_mask);
   int phase = 0;
@@ -305,7 +237,7 @@ __global__ void __launch_bounds__(kThreads) log_probs_kernel(const __grid_consta
       __syncthreads();
       if (a.tokens && threadIdx.x == 0)
         x = load_one<DT>(seg.at_column<DT>(v, static_cast<uint32_t>(token)));
-      st = row_stats<DT, TOP>(v, seg, lo, hi, cta, ctas, slots, phase, tops, a.batch_shift, thread_max);
+      st = row_stats<DT, true, TOP>(v, seg, lo, hi, cta, ctas, slots, phase, tops, a.entry_shift, thread_max);
     }
     if (threadIdx.x == 0 && cta == 0) {
       if (a.tokens) a.log_probs[t] = scored ? st.log_prob(x, v.inv_temp) : 0.f;
@@ -321,7 +253,7 @@ __global__ void __launch_bounds__(kThreads) log_probs_kernel(const __grid_consta
     int64_t* out_id = a.top_ids + t * k;
     int found = 0;
     if (scored && !st.bad()) {
-      select_top<DT>(v, seg, lo, hi, cta == 0, *top, k, tops, a.batch_shift, thread_max,
+      select_top<DT>(v, seg, lo, hi, cta == 0, *top, k, tops, a.entry_shift, thread_max,
                      !(fabsf(st.max) < -kClamp));
       const int mine = top->found;
       if (ctas == 1) {
@@ -369,14 +301,14 @@ __global__ void __launch_bounds__(kThreads) log_probs_kernel(const __grid_consta
 
 // ---------------------------------------------------------------- distillation
 template <int DT>
-__global__ void __launch_bounds__(kThreads) distill_kernel(const __grid_constant__ DistillArgs a) {
+__global__ void __launch_bounds__(kThreads, 5) distill_kernel(const __grid_constant__ DistillArgs a) {
   __shared__ Segments seg;
   __shared__ JoinSlots slots;
   __shared__ LossSlots loss;
   const VocabArgs& v = a.v;
   const uint32_t ctas = cluster_size(), cta = cluster_rank();
-  const uint32_t per = (v.cut.vectors + ctas - 1) / ctas;
-  const uint32_t lo = min(v.cut.vectors, cta * per), hi = min(v.cut.vectors, lo + per);
+  const uint32_t per = (v.cut.chunks + ctas - 1) / ctas;
+  const uint32_t lo = min(v.cut.chunks, cta * per), hi = min(v.cut.chunks, lo + per);
   start(ctas);
   if (threadIdx.x == 0) dev::record_sm(v.sm_mask);
   int phase = 0;
@@ -387,17 +319,17 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const __grid_constant
     const bool mine = cta == 0 && threadIdx.x < 32;
     if (mine) set_loss<DT>(v, seg, read_teacher(a, t), loss);
     float unused;
-    const Stats st = row_stats<DT, false>(v, seg, lo, hi, cta, ctas, slots, phase, nullptr, 0, unused);
+    const Stats st = row_stats<DT, false, false>(v, seg, lo, hi, cta, ctas, slots, phase, nullptr, 0, unused);
     if (mine) store_loss(a, t, loss, st);
   }
 }
 
 // CTAs of one row: as many as keep every SM at no more than four, but none
-// whose slice is less than one batch of every thread.
+// whose slice is less than one chunk of every warp.
 int cluster_for(const VocabArgs& v, const VocabLaunch& l) {
   int c = 1;
   while (c < kForwardCluster && v.rows * c * 2 <= static_cast<uint64_t>(l.sm_count) * 4 &&
-         v.cut.vectors >= static_cast<uint32_t>(2 * c * kThreads * kBatch) && (l.cap <= 0 || 2 * c <= l.cap))
+         v.cut.chunks >= static_cast<uint32_t>(2 * c * kThreads / 32) && (l.cap <= 0 || 2 * c <= l.cap))
     c *= 2;
   return c;
 }
@@ -412,15 +344,14 @@ uint64_t grid_for(const VocabArgs& v, const VocabLaunch& l, int cluster) {
 
 template <int DT, bool TOP>
 int launch_log_probs_t(LogProbsArgs& a, VocabLaunch& l) {
-  set_cut<DT>(a.v, kThreads, 0);
+  set_cut<DT>(a.v, 0);
   const int c = cluster_for(a.v, l);
   size_t smem = 0;
-  a.batches = a.batch_shift = 0;
+  a.entry_shift = 0;
   if (TOP) {
-    const uint32_t per = (a.v.cut.vectors + c - 1) / c;
-    a.batches = static_cast<int>((per + kThreads * kBatch - 1) / (kThreads * kBatch));
-    while (((a.batches + (1 << a.batch_shift) - 1) >> a.batch_shift) > kMaxEntries) ++a.batch_shift;
-    const int entries = (a.batches + (1 << a.batch_shift) - 1) >> a.batch_shift;
+    const uint32_t per = (a.v.cut.chunks + c - 1) / c, warps = kThreads / 32, most = (per + warps - 1) / warps;
+    while (((most + (1u << a.entry_shift) - 1) >> a.entry_shift) > kMaxEntries) ++a.entry_shift;
+    const uint32_t entries = (most + (1u << a.entry_shift) - 1) >> a.entry_shift;
     smem = sizeof(TopSlots) + (c > 1 ? sizeof(ClusterTop) : 0) + sizeof(uint16_t) * kThreads * entries;
     const cudaError_t e = cudaFuncSetAttribute(log_probs_kernel<DT, TOP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(smem));
@@ -431,7 +362,7 @@ int launch_log_probs_t(LogProbsArgs& a, VocabLaunch& l) {
 
 template <int DT>
 int launch_distill_t(DistillArgs& a, VocabLaunch& l) {
-  set_cut<DT>(a.v, kThreads, 0);
+  set_cut<DT>(a.v, 0);
   const int c = cluster_for(a.v, l);
   return launch_rows(distill_kernel<DT>, a, l, grid_for(a.v, l, c), kThreads, c, 0);
 }

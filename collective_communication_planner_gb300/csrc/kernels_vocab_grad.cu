@@ -8,7 +8,7 @@ namespace {
 using namespace vocab;
 
 constexpr int kThreads = 256;
-constexpr int kVecs = 8;  // vectors a thread holds
+constexpr uint64_t kKeepBytes = 40ull << 20;  // rows that L2 keeps between two reads
 
 // The segments of the current row for a gradient: where the logits and the
 // gradient start, and the first element of the body, which starts on a 16-byte
@@ -24,114 +24,106 @@ struct GradSegments : Segments {
 };
 
 template <int DT>
+__device__ __forceinline__ uint32_t head_of(const char* dst) {
+  return static_cast<uint32_t>(-reinterpret_cast<uintptr_t>(dst) & 15) / Elem<DT>::kBytes + Elem<DT>::kVec;
+}
+
+template <int DT>
 __device__ __forceinline__ void set_segments(const VocabArgs& v, uint64_t t, GradSegments& s) {
   if (threadIdx.x < v.used) {
     s.src[threadIdx.x] = static_cast<const char*>(v.p.src[threadIdx.x]) + t * v.src_stride * Elem<DT>::kBytes;
     char* dst = static_cast<char*>(v.p.dst[threadIdx.x]) + t * v.dst_stride * Elem<DT>::kBytes;
     s.dst[threadIdx.x] = dst;
-    const uint32_t gap = static_cast<uint32_t>(-reinterpret_cast<uintptr_t>(dst) & 15) / Elem<DT>::kBytes;
-    s.head[threadIdx.x] = v.aligned ? 0 : gap + Elem<DT>::kVec;
+    s.head[threadIdx.x] = v.aligned ? 0 : head_of<DT>(dst);
   }
 }
 
-// sixteen bytes from an address that is aligned to its elements only
-__device__ __forceinline__ uint4 load_any(const char* at) {
-  const uint32_t m = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(at) & 15);
-  if (m == 0) return dev::ld_global_v4(at);
-  const uint4 a = dev::ld_global_v4(at - m), b = dev::ld_global_v4(at - m + 16);
-  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  if (m & 8) {
-#pragma unroll
-    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
-  }
-  if (m & 4) {
-#pragma unroll
-    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
-  }
-  const uint32_t bits = (m & 3) * 8;
-  uint4 r;
-  r.x = __funnelshift_r(w[0], w[1], bits);
-  r.y = __funnelshift_r(w[1], w[2], bits);
-  r.z = __funnelshift_r(w[2], w[3], bits);
-  r.w = __funnelshift_r(w[3], w[4], bits);
-  return r;
-}
-
-// One row's gradient y = p (scale + slope log2 p), plus `hot` at `token`,
-// where p = 2^((x - max) c - log2_s).
+// One row's gradient y = p (scale + slope log2 p); columns that a token or a
+// teacher's entry names get their own term afterwards.
+// log2 p = x c - (max c + log2_s): the subtrahend is rounded once (hi), so
+// that it takes one fused operation an element, and what the rounding lost is
+// made up for in scale and slope. A row whose maximum is not within
+// (-2^100, 2^100) is not `fast`: (x - max) c - log2_s then.
 struct RowGrad {
-  float max, c, log2_s, scale, slope, hot;
-  uint32_t token;
+  float max, c, log2_s, hi, scale, slope, fast_scale, fast_slope;
   bool zero, fast;
 
-  __device__ __forceinline__ void set(const VocabArgs& v, float m, float log_s) {
+  __device__ __forceinline__ void set(const VocabArgs& v, float m, float log2_sum, float to_scale, float to_slope) {
     max = m;
     c = v.exp2_scale;
-    log2_s = log_s * kLog2e;
-    slope = hot = 0.f;
-    token = 0xFFFFFFFFu;
+    log2_s = log2_sum;
     fast = fabsf(m) < -kClamp;
+    scale = to_scale;
+    slope = to_slope;
+    const float mc = __fmul_rn(m, c);
+    hi = __fadd_rn(mc, log2_s);
+    // max c + log2_s - hi: the product's rounding, and the sum's (two-sum)
+    const float back = __fsub_rn(hi, mc);
+    const float lost = __fadd_rn(__fadd_rn(__fsub_rn(mc, __fsub_rn(hi, back)), __fsub_rn(log2_s, back)),
+                                 __fmaf_rn(m, c, -mc));
+    const float f = exp2_ftz(-lost);
+    fast_scale = f * __fmaf_rn(-slope, lost, scale);
+    fast_slope = f * slope;
   }
-  __device__ __forceinline__ float one(float x, uint32_t column) const {
-    const float l = (x - max) * c - log2_s, p = exp2_ftz(l);
+  __device__ __forceinline__ float one(float x) const {
+    const float l = fast ? __fmaf_rn(x, c, -hi) : (x - max) * c - log2_s, p = exp2_ftz(l);
+    const float s = fast ? fast_slope : slope, o = fast ? fast_scale : scale;
     // a masked place: 0 whatever its distance
-    float y = p == 0.f ? 0.f : p * (slope == 0.f ? scale : __fmaf_rn(slope, l, scale));
-    if (column == token) y += hot;
-    return y;
+    return p == 0.f ? 0.f : p * (s == 0.f ? o : __fmaf_rn(s, l, o));
   }
   template <bool SLOPE>
   __device__ __forceinline__ f32x2 two(f32x2 x) const {
-    const f32x2 l = fma2(add2(x, pack(-max, -max)), pack(c, c), pack(-log2_s, -log2_s));
+    const f32x2 l = fma2(x, pack(c, c), pack(-hi, -hi));
     const f32x2 p = exp2x2(l);
-    if (!SLOPE) return mul2(p, pack(scale, scale));
-    return mul2(p, fma2(pack(slope, slope), l, pack(scale, scale)));
+    if (!SLOPE) return mul2(p, pack(fast_scale, fast_scale));
+    return mul2(p, fma2(pack(fast_slope, fast_slope), l, pack(fast_scale, fast_scale)));
   }
 };
 
-// The gradient of N vectors already in registers (clamped where the row is
-// `fast`), stored; the vectors a thread holds are Walk's from `first`.
-template <int DT, int N, bool SLOPE>
-__device__ __forceinline__ void store_vectors(const VocabArgs& v, const GradSegments& s, const RowGrad& g,
-                                              Vec<DT> (&x)[N], uint32_t first, uint32_t hi) {
-  constexpr int K = Elem<DT>::kVec;
-  Walk w(v.cut, first);
+// The gradient of a vector of the row. A named column's own term is not in it:
+// a branch for it here would keep the vectors of a chunk from overlapping
+// (GB300, 4096 x 131072 bf16: 452 us with it, 314 without).
+template <int DT, bool SLOPE>
+__device__ __forceinline__ uint4 grad_of(const RowGrad& g, Vec<DT>& x) {
+  Vec<DT> y;
+  if (g.fast) {
+    if (SLOPE) x.clamp();  // a masked place: 0 times a finite distance
 #pragma unroll
-  for (int k = 0; k < N; ++k, w.next(v.cut)) {
-    if (w.index >= hi) break;
-    const uint32_t col = s.head[w.seg] + w.vec * K;
-    const uint32_t hot = g.token - (w.seg * v.shard + col);
-    Vec<DT> y;
-    if (g.fast) {
-      f32x2 r[Vec<DT>::kPairs];
+    for (int i = 0; i < Vec<DT>::kPairs; ++i) y.put_pair(i, g.two<SLOPE>(x.pair(i)));
+  } else {
 #pragma unroll
-      for (int i = 0; i < Vec<DT>::kPairs; ++i) r[i] = g.two<SLOPE>(x[k].pair(i));
-      if (hot < K) {
+    for (int i = 0; i < Vec<DT>::kPairs; ++i) y.put_pair(i, pack(g.one(x.get(2 * i)), g.one(x.get(2 * i + 1))));
+  }
+  return y.out();
+}
+
+// The gradient of this warp's chunks of [lo, hi) of the row. In place a lane
+// reads a vector before it replaces it, and no other lane reads it: the
+// buffers are equally aligned then.
+template <int DT, bool SLOPE>
+__device__ __forceinline__ void store_chunks(const VocabArgs& v, const GradSegments& s, const RowGrad& g, uint32_t lo,
+                                             uint32_t hi) {
+  for (ChunkWalk w(v.cut, lo + (threadIdx.x >> 5)); w.index < hi; w.next(v.cut)) {
+    Vec<DT> x[kBatch];
+    const uint32_t first = w.vector(), end = w.vectors(v), head = s.head[w.seg];
+    load_chunk<DT, true>(v, s.at<DT>(w.seg, head), w, x, StreamLoad());
+    char* to = s.to<DT>(w.seg, head) + static_cast<uint64_t>(first) * 16;
 #pragma unroll
-        for (int i = 0; i < Vec<DT>::kPairs; ++i)
-          if (i == hot / 2) r[i] = add2(r[i], hot & 1 ? pack(0.f, g.hot) : pack(g.hot, 0.f));
-      }
-#pragma unroll
-      for (int i = 0; i < Vec<DT>::kPairs; ++i) y.put_pair(i, r[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < Vec<DT>::kPairs; ++i)
-        y.put_pair(i, pack(g.one(x[k].get(2 * i), w.seg * v.shard + col + 2 * i),
-                           g.one(x[k].get(2 * i + 1), w.seg * v.shard + col + 2 * i + 1)));
+    for (int k = 0; k < kBatch; ++k) {
+      if (first + k * 32 >= end) break;
+      dev::st_global_v4(to + k * 512, grad_of<DT, SLOPE>(g, x[k]));
     }
-    dev::st_global_v4(s.to<DT>(w.seg, col), y.out());
   }
 }
 
-template <int DT, int N>
-__device__ __forceinline__ void load_vectors(const VocabArgs& v, const GradSegments& s, Vec<DT> (&x)[N],
-                                             uint32_t first, uint32_t hi) {
-  Walk w(v.cut, first);
+template <int DT>
+__device__ __forceinline__ void zero_chunks(const VocabArgs& v, const GradSegments& s, uint32_t lo, uint32_t hi) {
+  for (ChunkWalk w(v.cut, lo + (threadIdx.x >> 5)); w.index < hi; w.next(v.cut)) {
+    const uint32_t first = w.vector(), end = w.vectors(v);
+    char* to = s.to<DT>(w.seg, s.head[w.seg]) + static_cast<uint64_t>(first) * 16;
 #pragma unroll
-  for (int k = 0; k < N; ++k, w.next(v.cut)) {
-    x[k].set_empty();
-    if (w.index >= hi) continue;
-    const char* at = s.at<DT>(w.seg, s.head[w.seg] + w.vec * Elem<DT>::kVec);
-    x[k].set(v.aligned ? dev::ld_global_v4(at) : load_any(at));
+    for (int k = 0; k < kBatch; ++k)
+      if (first + k * 32 < end) dev::st_global_v4(to + k * 512, make_uint4(0, 0, 0, 0));
   }
 }
 
@@ -143,7 +135,7 @@ __device__ __forceinline__ void store_edges(const VocabArgs& v, const GradSegmen
   for (uint32_t e = threadIdx.x; cta == 0 && e < v.cut.edges; e += blockDim.x) {
     uint32_t seg, col;
     edge_at<DT>(v, s, e, seg, col);
-    store_one<DT>(s.to<DT>(seg, col), g.zero ? 0.f : g.one(load_one<DT>(s.at<DT>(seg, col)), seg * v.shard + col));
+    store_one<DT>(s.to<DT>(seg, col), g.zero ? 0.f : g.one(load_one<DT>(s.at<DT>(seg, col))));
   }
   const uint32_t all = v.nranks * v.shard;
   for (uint32_t j = v.vocab + cta * blockDim.x + threadIdx.x; j < all; j += ctas * blockDim.x) {
@@ -152,53 +144,81 @@ __device__ __forceinline__ void store_edges(const VocabArgs& v, const GradSegmen
   }
 }
 
-template <int DT, int N>
-__device__ __forceinline__ void store_zeros(const VocabArgs& v, const GradSegments& s, uint32_t first, uint32_t hi) {
-  Walk w(v.cut, first);
-#pragma unroll
-  for (int k = 0; k < N; ++k, w.next(v.cut))
-    if (w.index < hi)
-      dev::st_global_v4(s.to<DT>(w.seg, s.head[w.seg] + w.vec * Elem<DT>::kVec), make_uint4(0, 0, 0, 0));
+// Work item b of a call is part b % parts of row b / parts: an equal share of its chunks.
+struct Item {
+  uint64_t row;
+  uint32_t part, lo, hi;
+  __device__ __forceinline__ Item(const VocabArgs& v, uint64_t b, uint32_t parts) {
+    row = b >> 32 ? b / parts : static_cast<uint32_t>(b) / parts;
+    part = static_cast<uint32_t>(b - row * parts);
+    const uint32_t per = (v.cut.chunks + parts - 1) / parts;
+    lo = min(v.cut.chunks, part * per);
+    hi = min(v.cut.chunks, lo + per);
+  }
+};
+
+
+// the chunk that a column of row t is in, or kEdge
+constexpr uint32_t kEdge = 0xFFFFFFFFu;
+template <int DT>
+__device__ __forceinline__ uint32_t chunk_of(const VocabArgs& v, uint64_t t, uint32_t column) {
+  const uint32_t seg = column / v.shard, col = column - seg * v.shard;
+  const char* dst = static_cast<const char*>(v.p.dst[seg]) + t * v.dst_stride * Elem<DT>::kBytes;
+  const uint32_t head = v.aligned ? 0 : head_of<DT>(dst);
+  const uint32_t vectors = seg + 1 == v.used ? v.cut.last : v.cut.full, vec = (col - head) / Elem<DT>::kVec;
+  if (col < head || vec >= vectors) return kEdge;
+  return seg * v.cut.per_segment + vec / kChunkVectors;
 }
 
-// Pieces of rows: CTA b takes piece b % pieces of row b / pieces.
+// whether a CTA that has chunks [lo, hi) of row t, and with `edges` the edge
+// elements, has a column
+template <int DT>
+__device__ __forceinline__ bool has_column(const VocabArgs& v, uint64_t t, uint32_t column, uint32_t lo, uint32_t hi,
+                                           bool edges) {
+  const uint32_t chunk = chunk_of<DT>(v, t, column);
+  return chunk == kEdge ? edges : chunk >= lo && chunk < hi;
+}
+
+template <int DT>
+__device__ __forceinline__ float read_column(const VocabArgs& v, uint64_t t, uint32_t column) {
+  const uint32_t seg = column / v.shard;
+  return load_one<DT>(static_cast<const char*>(v.p.src[seg]) +
+                      (t * v.src_stride + column - seg * v.shard) * Elem<DT>::kBytes);
+}
+template <int DT>
+__device__ __forceinline__ void write_column(const VocabArgs& v, uint64_t t, uint32_t column, float y) {
+  const uint32_t seg = column / v.shard;
+  store_one<DT>(static_cast<char*>(v.p.dst[seg]) + (t * v.dst_stride + column - seg * v.shard) * Elem<DT>::kBytes, y);
+}
+
 template <int DT, bool SLOPE>
-__global__ void __launch_bounds__(kThreads) log_probs_grad_kernel(const __grid_constant__ LogProbsGradArgs a) {
+__global__ void __launch_bounds__(kThreads, 5) log_probs_grad_kernel(const __grid_constant__ LogProbsGradArgs a) {
   __shared__ GradSegments seg;
   const VocabArgs& v = a.v;
-  const uint32_t pieces = max(1u, (v.cut.vectors + kThreads * kVecs - 1) / (kThreads * kVecs));
   start(1);
   if (threadIdx.x == 0) dev::record_sm(v.sm_mask);
-  for (uint64_t b = blockIdx.x; b < v.rows * pieces; b += gridDim.x) {
-    const uint64_t t = b / pieces;
-    const uint32_t piece = static_cast<uint32_t>(b - t * pieces), first = piece * kThreads * kVecs + threadIdx.x;
-    __syncthreads();  // the last piece's segments are done with
-    set_segments<DT>(v, t, seg);
+  for (uint64_t b = blockIdx.x; b < v.rows * v.parts; b += gridDim.x) {
+    const Item it(v, b, v.parts);
+    const uint64_t t = it.row;
+    set_segments<DT>(v, t, seg);  // the last item's are done with: the barrier below
     const int64_t token = a.tokens[t];
-    const float da = a.d_log_probs[t], db = SLOPE ? a.d_entropy[t] : 0.f;
+    const float da = a.d_log_probs[t], db = SLOPE ? a.d_entropy[t] : 0.f, m = a.stats[2 * t];
+    const float ls = a.stats[2 * t + 1], h = SLOPE && db != 0.f ? a.entropy[t] : 0.f;
     RowGrad g;
-    g.set(v, a.stats[2 * t], a.stats[2 * t + 1]);
-    g.zero = token < 0 || token >= v.vocab || (da == 0.f && db == 0.f) || g.max == -INFINITY;
-    g.scale = -da * v.inv_temp;
-    if (SLOPE && db != 0.f) {
-      // log p in base 2: log p = ln 2 log2 p
-      g.scale = -(da + db * a.entropy[t]) * v.inv_temp;
-      g.slope = -db * v.inv_temp * kLn2;
-    }
-    g.hot = da * v.inv_temp;
-    g.token = static_cast<uint32_t>(token);
+    // log p in base 2: log p = ln 2 log2 p
+    g.set(v, m, ls * kLog2e, -(da + db * h) * v.inv_temp, -db * v.inv_temp * kLn2);
+    g.zero = token < 0 || token >= v.vocab || (da == 0.f && db == 0.f) || m == -INFINITY;
+    // thread 0 gives the token's column its own term after the body's stores;
+    // it reads the logit first, since an in-place gradient replaces it
+    const uint32_t column = static_cast<uint32_t>(token);
+    const bool named = threadIdx.x == 0 && !g.zero && has_column<DT>(v, t, column, it.lo, it.hi, it.part == 0);
+    const float x = named ? read_column<DT>(v, t, column) : 0.f;
     __syncthreads();
-    if (g.zero) {
-      store_zeros<DT, kVecs>(v, seg, first, v.cut.vectors);
-    } else {
-      Vec<DT> x[kVecs];
-      load_vectors<DT, kVecs>(v, seg, x, first, v.cut.vectors);
-      if (SLOPE && g.fast)
-#pragma unroll
-        for (int k = 0; k < kVecs; ++k) x[k].clamp();
-      store_vectors<DT, kVecs, SLOPE>(v, seg, g, x, first, v.cut.vectors);
-    }
-    store_edges<DT>(v, seg, g, t, piece, pieces);
+    if (g.zero) zero_chunks<DT>(v, seg, it.lo, it.hi);
+    else store_chunks<DT, SLOPE>(v, seg, g, it.lo, it.hi);
+    store_edges<DT>(v, seg, g, t, it.part, v.parts);
+    __syncthreads();
+    if (named) write_column<DT>(v, t, column, g.one(x) + da * v.inv_temp);
   }
 }
 
@@ -212,32 +232,22 @@ struct Named {
   int count;
 };
 
-// Warp 0 keeps the entries of the row whose column belongs to vectors
-// [lo, hi), or, for CTA `cta` of `ctas`, to its edge elements. Reads the
-// logits there, since an in-place gradient replaces them.
+// Warp 0 keeps the entries of the row whose column is in chunks [lo, hi), or,
+// with `edges`, an edge element, in entry order, with the logits there, since an
+// in-place gradient replaces them.
 template <int DT>
-__device__ __forceinline__ void keep_named(const VocabArgs& v, const GradSegments& s, const TeacherRow& r, Named& n,
-                                           uint32_t lo, uint32_t hi, uint32_t cta) {
-  constexpr int K = Elem<DT>::kVec;
+__device__ __forceinline__ void keep_named(const VocabArgs& v, uint64_t t, const TeacherRow& r, Named& n, uint32_t lo,
+                                           uint32_t hi, bool edges) {
   int count = 0;
 #pragma unroll
   for (int i = 0; i < kMaxTop / 32; ++i) {
-    bool here = false;
-    uint32_t seg = 0, col = 0;
-    if (r.column[i] >= 0) {
-      seg = r.column[i] / v.shard;
-      col = r.column[i] - seg * v.shard;
-      const uint32_t vec = (col - s.head[seg]) / K;  // huge before the head
-      const uint32_t vectors = seg + 1 == v.used ? v.cut.last : v.cut.full;
-      if (col < s.head[seg] || vec >= vectors) here = cta == 0;
-      else here = seg * v.cut.full + vec >= lo && seg * v.cut.full + vec < hi;
-    }
+    const bool here = r.column[i] >= 0 && has_column<DT>(v, t, r.column[i], lo, hi, edges);
     const uint32_t mask = __ballot_sync(0xFFFFFFFFu, here);
     if (here) {
       const int at = count + __popc(mask & ((1u << (threadIdx.x & 31)) - 1));
       n.column[at] = r.column[i];
       n.q[at] = r.q[i];
-      n.x[at] = load_one<DT>(s.at<DT>(seg, col));
+      n.x[at] = read_column<DT>(v, t, r.column[i]);
     }
     count += __popc(mask);
   }
@@ -249,8 +259,7 @@ __device__ __forceinline__ void keep_named(const VocabArgs& v, const GradSegment
 
 // after a barrier behind the body's stores
 template <int DT>
-__device__ __forceinline__ void store_named(const VocabArgs& v, const GradSegments& s, const Named& n, RowGrad g,
-                                            float weight) {
+__device__ __forceinline__ void store_named(const VocabArgs& v, uint64_t t, const Named& n, const RowGrad& g, float weight) {
   const int i = threadIdx.x;
   if (i >= n.count) return;
   const int32_t column = n.column[i];
@@ -260,70 +269,54 @@ __device__ __forceinline__ void store_named(const VocabArgs& v, const GradSegmen
     if (j < i) return;  // an earlier entry names it too and does this
     q += n.q[j];
   }
-  const uint32_t seg = column / v.shard, col = column - seg * v.shard;
-  g.hot = -q * weight;
-  g.token = column;
-  store_one<DT>(s.to<DT>(seg, col), g.one(n.x[i], column));
+  write_column<DT>(v, t, column, g.one(n.x[i]) - q * weight);
 }
 
 template <int DT>
-__global__ void __launch_bounds__(kThreads) distill_grad_kernel(const __grid_constant__ DistillArgs a) {
+__global__ void __launch_bounds__(kThreads, 5) distill_grad_kernel(const __grid_constant__ DistillArgs a) {
   __shared__ GradSegments seg;
   __shared__ Named named;
   const VocabArgs& v = a.v;
-  const uint32_t pieces = max(1u, (v.cut.vectors + kThreads * kVecs - 1) / (kThreads * kVecs));
   start(1);
   if (threadIdx.x == 0) dev::record_sm(v.sm_mask);
-  for (uint64_t b = blockIdx.x; b < v.rows * pieces; b += gridDim.x) {
-    const uint64_t t = b / pieces;
-    const uint32_t piece = static_cast<uint32_t>(b - t * pieces);
-    const uint32_t lo = piece * kThreads * kVecs, first = lo + threadIdx.x;
-    const uint32_t hi = min(v.cut.vectors, lo + kThreads * kVecs);
-    __syncthreads();  // the last piece's segments and columns are done with
+  for (uint64_t b = blockIdx.x; b < v.rows * v.parts; b += gridDim.x) {
+    const Item it(v, b, v.parts);
+    const uint64_t t = it.row;
+    const float w = a.weights[t] * v.inv_temp, m = a.saved[2 * t], ls = a.saved[2 * t + 1];
+    bool zero = w == 0.f || m == -INFINITY;
+    __syncthreads();  // the last item's segments and columns are done with
     set_segments<DT>(v, t, seg);
-    const float w = a.weights[t] * v.inv_temp;
+    if (!zero && threadIdx.x < 32) keep_named<DT>(v, t, read_teacher(a, t), named, it.lo, it.hi, it.part == 0);
+    __syncthreads();
+    zero = zero || named.total == 0.f;
     RowGrad g;
-    g.set(v, a.saved[2 * t], a.saved[2 * t + 1]);
-    g.zero = w == 0.f || g.max == -INFINITY;
-    __syncthreads();
-    Vec<DT> x[kVecs];
-    if (!g.zero) {
-      load_vectors<DT, kVecs>(v, seg, x, first, hi);
-      if (threadIdx.x < 32) keep_named<DT>(v, seg, read_teacher(a, t), named, lo, hi, piece);
-    }
-    __syncthreads();
-    if (!g.zero) {
-      g.scale = w * named.total;
-      g.zero = named.total == 0.f;
-    }
-    if (g.zero) store_zeros<DT, kVecs>(v, seg, first, hi);
-    else store_vectors<DT, kVecs, false>(v, seg, g, x, first, hi);
-    store_edges<DT>(v, seg, g, t, piece, pieces);
-    if (!g.zero) {
+    g.set(v, m, ls * kLog2e, w * named.total, 0.f);
+    g.zero = zero;
+    if (zero) zero_chunks<DT>(v, seg, it.lo, it.hi);
+    else store_chunks<DT, false>(v, seg, g, it.lo, it.hi);
+    store_edges<DT>(v, seg, g, t, it.part, v.parts);
+    if (!zero) {
       __syncthreads();
-      store_named<DT>(v, seg, named, g, w);
+      store_named<DT>(v, t, named, g, w);
     }
   }
 }
 
-constexpr int kStepThreads = 512;
 constexpr int kStepCluster = 8;
 
-// Loss and gradient in one call: a cluster of CTAs holds a row in registers,
-// joins its statistics through distributed shared memory and writes the
-// gradient, so that a logit is read once. A row that is longer than the
-// cluster's registers (or its CTAs, under a cap) is taken in several tiles and
-// read a second time for the gradient.
+// Loss and gradient in one call: a cluster of CTAs sums up a row, joins its
+// statistics through distributed shared memory and reads it again, from L2,
+// for the gradient.
 template <int DT>
-__global__ void __launch_bounds__(kStepThreads, 2) distill_step_kernel(const __grid_constant__ DistillArgs a) {
+__global__ void __launch_bounds__(kThreads, 5) distill_step_kernel(const __grid_constant__ DistillArgs a) {
   __shared__ GradSegments seg;
   __shared__ Named named;
   __shared__ LossSlots loss;
   __shared__ JoinSlots slots;
   const VocabArgs& v = a.v;
   const uint32_t ctas = cluster_size(), cta = cluster_rank();
-  const uint32_t tile = blockDim.x * kVecs, tiles = max(1u, (v.cut.vectors + tile * ctas - 1) / (tile * ctas));
-  const uint32_t lo = min(v.cut.vectors, cta * tile * tiles), hi = min(v.cut.vectors, lo + tile * tiles);
+  const uint32_t per = (v.cut.chunks + ctas - 1) / ctas;
+  const uint32_t lo = min(v.cut.chunks, cta * per), hi = min(v.cut.chunks, lo + per);
   start(ctas);
   if (threadIdx.x == 0) dev::record_sm(v.sm_mask);
   int phase = 0;
@@ -332,76 +325,44 @@ __global__ void __launch_bounds__(kStepThreads, 2) distill_step_kernel(const __g
     __syncthreads();  // the last row's segments and columns are done with
     set_segments<DT>(v, t, seg);
     __syncthreads();
-    Vec<DT> x[kVecs];
-    load_vectors<DT, kVecs>(v, seg, x, lo + threadIdx.x, hi);
     if (threadIdx.x < 32) {
       const TeacherRow q = read_teacher(a, t);
-      keep_named<DT>(v, seg, q, named, lo, hi, cta);
+      keep_named<DT>(v, t, q, named, lo, hi, cta == 0);
       if (cta == 0) set_loss<DT>(v, seg, q, loss);
     }
-    // the thread's maximum so far, and the sum relative to it
-    Part p{kClamp, 0.f, 0.f};
-    for (uint32_t i = 0;;) {
-#pragma unroll
-      for (int k = 0; k < kVecs; ++k) x[k].clamp();
-      const float top = batch_max<DT, kVecs>(x);
-      if (top > p.m) rebase(p, top, c);
-      const float r = __fmul_rn(p.m, c);
-      f32x2 s[2] = {0, 0};
-#pragma unroll
-      for (int k = 0; k < kVecs; ++k)
-#pragma unroll
-        for (int j = 0; j < Vec<DT>::kPairs; ++j)
-          s[j & 1] = add2(s[j & 1], exp2x2(fma2(x[k].pair(j), pack(c, c), pack(-r, -r))));
-      float s0, s1, s2, s3;
-      unpack(s[0], s0, s1);
-      unpack(s[1], s2, s3);
-      p.s += (s0 + s1) + (s2 + s3);
-      if (++i == tiles) break;
-      load_vectors<DT, kVecs>(v, seg, x, lo + i * tile + threadIdx.x, hi);
-    }
-    for (uint32_t e = threadIdx.x; cta == 0 && e < v.cut.edges; e += blockDim.x) {
-      uint32_t es, ec;
-      edge_at<DT>(v, seg, e, es, ec);
-      const float y = max_f32(load_one<DT>(seg.at<DT>(es, ec)), kClamp);
-      if (y > p.m) rebase(p, y, c);
-      p.s += exp2_ftz(__fmaf_rn(y, c, -__fmul_rn(p.m, c)));
-    }
+    Part p = scan_row<DT, false, true>(v, seg, lo, hi, cta == 0, KeepLoad(), [](float) {});
     p = row_join(p, c, slots, phase, ctas);
     const bool fast = fabsf(p.m) < -kClamp;
     const Stats st = fast ? stats_of(p, c) : slow_stats<DT>(v, seg, lo, hi, slots, phase, cta, ctas);
     if (cta == 0 && threadIdx.x < 32) store_loss(a, t, loss, st);
     const float w = a.weights[t] * v.inv_temp;
     RowGrad g;
-    g.set(v, st.max, 0.f);
-    g.log2_s = st.log2_s;
-    g.scale = w * named.total;
+    g.set(v, st.max, st.log2_s, w * named.total, 0.f);
     g.zero = w == 0.f || named.total == 0.f || st.empty();
     // An in-place gradient may be written from here on: past the join's
     // barrier a CTA reads its own columns only, each before it replaces it.
-    for (uint32_t i = 0; i < tiles; ++i) {
-      const uint32_t first = lo + i * tile + threadIdx.x;
-      if (g.zero) {
-        store_zeros<DT, kVecs>(v, seg, first, hi);
-        continue;
-      }
-      // one tile is still in registers, but clamped
-      if (tiles > 1 || !fast) load_vectors<DT, kVecs>(v, seg, x, first, hi);
-      store_vectors<DT, kVecs, false>(v, seg, g, x, first, hi);
-    }
+    if (g.zero) zero_chunks<DT>(v, seg, lo, hi);
+    else store_chunks<DT, false>(v, seg, g, lo, hi);
     store_edges<DT>(v, seg, g, t, cta, ctas);
     if (!g.zero) {
       __syncthreads();
-      store_named<DT>(v, seg, named, g, w);
+      store_named<DT>(v, t, named, g, w);
     }
   }
 }
 
-template <typename Args>
-int launch_pieces(void (*kernel)(Args), const Args& a, VocabLaunch& l) {
-  const VocabArgs& v = a.v;
-  const uint64_t pieces = v.cut.vectors ? (v.cut.vectors + kThreads * kVecs - 1) / (kThreads * kVecs) : 1;
-  uint64_t grid = v.rows * pieces;
+template <int DT, typename Args>
+int launch_parts(void (*kernel)(Args), Args& a, VocabLaunch& l) {
+  VocabArgs& v = a.v;
+  set_cut<DT>(v, 2);
+  // an item is at most eight chunks a warp; fewer where that leaves SMs
+  // without four items
+  constexpr uint32_t kWarps = kThreads / 32;
+  uint32_t deep = 8;
+  while (deep > 1 && v.rows * ((v.cut.chunks + deep * kWarps - 1) / (deep * kWarps)) < static_cast<uint64_t>(l.sm_count) * 4)
+    deep /= 2;
+  v.parts = v.cut.chunks > deep * kWarps ? (v.cut.chunks + deep * kWarps - 1) / (deep * kWarps) : 1;
+  uint64_t grid = v.rows * v.parts;
   const uint64_t most = l.cap > 0 ? static_cast<uint64_t>(l.cap) : static_cast<uint64_t>(1) << 30;
   if (grid > most) grid = most;
   return launch_rows(kernel, a, l, grid, kThreads, 1, 0);
@@ -409,29 +370,29 @@ int launch_pieces(void (*kernel)(Args), const Args& a, VocabLaunch& l) {
 
 template <int DT>
 int launch_step_t(DistillArgs& a, VocabLaunch& l) {
-  // the smallest cluster whose registers hold a row, then the smallest CTAs
-  set_cut<DT>(a.v, kStepThreads, 2);
-  const uint32_t n = a.v.cut.vectors;
+  VocabArgs& v = a.v;
+  set_cut<DT>(v, 2);
+  // CTAs of a row: few enough rows at once for L2 to keep them between the two
+  // reads, or as many as the SMs take of few rows; every warp gets a chunk
+  const uint64_t row_bytes = static_cast<uint64_t>(v.vocab) * Elem<DT>::kBytes;
+  const uint64_t resident = static_cast<uint64_t>(l.sm_count) * 4;
   int c = 1;
-  while (c < kStepCluster && static_cast<uint32_t>(c * kStepThreads * kVecs) < n && (l.cap <= 0 || 2 * c <= l.cap)) c *= 2;
-  const uint32_t per = (n + c * kVecs - 1) / (c * kVecs);
-  const int threads = per >= kStepThreads ? kStepThreads : per <= 128 ? 128 : static_cast<int>((per + 31) / 32 * 32);
-  set_cut<DT>(a.v, threads, 2);
-  uint64_t rows = a.v.rows;
+  while (c < kStepCluster && v.cut.chunks >= static_cast<uint32_t>(2 * c * kThreads / 32) &&
+         (l.cap <= 0 || 2 * c <= l.cap) &&
+         (v.rows * 2 * c <= resident || (v.rows * c > resident && resident / c * row_bytes > kKeepBytes)))
+    c *= 2;
+  uint64_t rows = v.rows;
   if (l.cap > 0 && rows * c > static_cast<uint64_t>(l.cap)) rows = l.cap / c;
   const uint64_t most = static_cast<uint64_t>(1) << 27;
-  return launch_rows(distill_step_kernel<DT>, a, l, (rows < most ? rows : most) * c, threads, c, 0);
+  return launch_rows(distill_step_kernel<DT>, a, l, (rows < most ? rows : most) * c, kThreads, c, 0);
 }
 
 }  // namespace
 
 int launch_log_probs_grad(int dtype, LogProbsGradArgs& a, VocabLaunch& l) {
-  if (dtype == kBF16) {
-    set_cut<kBF16>(a.v, kThreads, 2);
-    return launch_pieces(a.d_entropy ? log_probs_grad_kernel<kBF16, true> : log_probs_grad_kernel<kBF16, false>, a, l);
-  }
-  set_cut<kF32>(a.v, kThreads, 2);
-  return launch_pieces(a.d_entropy ? log_probs_grad_kernel<kF32, true> : log_probs_grad_kernel<kF32, false>, a, l);
+  if (dtype == kBF16)
+    return launch_parts<kBF16>(a.d_entropy ? log_probs_grad_kernel<kBF16, true> : log_probs_grad_kernel<kBF16, false>, a, l);
+  return launch_parts<kF32>(a.d_entropy ? log_probs_grad_kernel<kF32, true> : log_probs_grad_kernel<kF32, false>, a, l);
 }
 
 int launch_distill(int dtype, DistillArgs& a, VocabLaunch& l) {
@@ -440,12 +401,8 @@ int launch_distill(int dtype, DistillArgs& a, VocabLaunch& l) {
 }
 
 int launch_distill_grad(int dtype, DistillArgs& a, VocabLaunch& l) {
-  if (dtype == kBF16) {
-    set_cut<kBF16>(a.v, kThreads, 2);
-    return launch_pieces(distill_grad_kernel<kBF16>, a, l);
-  }
-  set_cut<kF32>(a.v, kThreads, 2);
-  return launch_pieces(distill_grad_kernel<kF32>, a, l);
+  return dtype == kBF16 ? launch_parts<kBF16>(distill_grad_kernel<kBF16>, a, l)
+                        : launch_parts<kF32>(distill_grad_kernel<kF32>, a, l);
 }
 
 }  // namespace tccl

@@ -8,16 +8,18 @@ namespace tccl {
 constexpr int kMaxTop = 128;
 
 // How the row kernels walk a row. Every rank's segment of a row is cut into
-// 16-byte vectors plus edge elements, with the same number of vectors in
-// every full segment, so that one index runs over the vectors of all ranks.
+// 16-byte vectors, the same number in every full segment, plus edge elements.
+// Vectors go to warps in chunks of kChunkVectors (the last of a segment may be
+// short), counted through the segments, so that short segments keep all warps
+// busy as well and a lane's vectors lie at fixed distances from one address.
+constexpr int kBatch = 4;                   // vectors a lane takes of a chunk
+constexpr int kChunkVectors = 32 * kBatch;
 struct VocabCut {
-  uint32_t full, last; // vectors of a full segment, of the last one
-  uint32_t divisor;    // full, but at least 1
-  uint32_t vectors;    // vectors of a row
-  uint32_t edge;       // edge elements of a full segment
-  uint32_t edges;      // edge elements of a row
-  // a step of `threads` vectors in (segment, vector) form
-  uint32_t step_seg, step_vec;
+  uint32_t full, last;   // vectors of a full segment, of the last one
+  uint32_t per_segment;  // chunks of a full segment, at least 1
+  uint32_t chunks;       // chunks of a row
+  uint32_t edge, edges;  // edge elements of a full segment, of a row
+  uint32_t step_seg, step_part;  // a step of one chunk per warp of a CTA, in (segment, chunk) form
 };
 
 // A [rows, vocab] matrix of logits cut by columns over `used` rank buffers.
@@ -29,6 +31,7 @@ struct VocabArgs {
   uint32_t vocab, shard;
   int nranks;
   int used;         // ranks that hold valid columns
+  uint32_t parts;   // gradients apart: work items of a row
   int aligned;      // every row of every buffer starts on a 16-byte boundary
   float inv_temp;   // 1 / temperature
   float exp2_scale; // log2(e) / temperature
@@ -42,8 +45,7 @@ struct LogProbsArgs {
   float* top_log_probs;
   int64_t* top_ids;
   int top_k;
-  int batches;      // batches of vectors a thread takes of its slice
-  int batch_shift;  // 2^batch_shift batches share one stored maximum
+  int entry_shift;  // 2^entry_shift chunks share one stored maximum
 };
 
 struct LogProbsGradArgs {

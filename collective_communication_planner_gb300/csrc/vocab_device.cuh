@@ -297,21 +297,83 @@ __device__ __forceinline__ void set_segments(const VocabArgs& v, uint64_t t, Seg
   }
 }
 
-// The vectors first, first + blockDim, ... of a row, in (segment, vector) form.
-struct Walk {
-  uint32_t index, seg, vec;
-  __device__ __forceinline__ Walk(const VocabCut& c, uint32_t first)
-      : index(first), seg(first / c.divisor), vec(first - seg * c.divisor) {}
+// The chunks `first`, `first` + warps of the CTA, ... of a row.
+struct ChunkWalk {
+  uint32_t index, seg, part;
+  __device__ __forceinline__ ChunkWalk(const VocabCut& c, uint32_t first)
+      : index(first), seg(first / c.per_segment), part(first - seg * c.per_segment) {}
   __device__ __forceinline__ void next(const VocabCut& c) {
-    index += blockDim.x;
+    index += blockDim.x >> 5;
     seg += c.step_seg;
-    vec += c.step_vec;
-    if (vec >= c.divisor) {
-      vec -= c.divisor;
+    part += c.step_part;
+    if (part >= c.per_segment) {
+      part -= c.per_segment;
       ++seg;
     }
   }
+  // this lane's first vector in the segment, and the segment's vectors
+  __device__ __forceinline__ uint32_t vector() const { return part * kChunkVectors + (threadIdx.x & 31); }
+  __device__ __forceinline__ uint32_t vectors(const VocabArgs& v) const {
+    return seg + 1 == v.used ? v.cut.last : v.cut.full;
+  }
 };
+
+// Loads that stream: every byte is used once.
+struct StreamLoad {
+  __device__ __forceinline__ uint4 operator()(const char* at) const { return dev::ld_global_v4(at); }
+};
+// A first read of what is read again.
+struct KeepLoad {
+  __device__ __forceinline__ uint4 operator()(const char* at) const { return *reinterpret_cast<const uint4*>(at); }
+};
+
+// sixteen bytes from an address that is not on a 16-byte boundary
+template <typename Load>
+__device__ __forceinline__ uint4 load_any(const char* at, Load load) {
+  const uint32_t m = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(at) & 15);
+  const uint4 a = load(at - m), b = load(at - m + 16);
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  if (m & 8) {
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+  }
+  if (m & 4) {
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+  }
+  const uint32_t bits = (m & 3) * 8;
+  uint4 r;
+  r.x = __funnelshift_r(w[0], w[1], bits);
+  r.y = __funnelshift_r(w[1], w[2], bits);
+  r.z = __funnelshift_r(w[2], w[3], bits);
+  r.w = __funnelshift_r(w[3], w[4], bits);
+  return r;
+}
+
+template <int DT, typename Load>
+__device__ __forceinline__ void load_vectors(const char* at, uint32_t first, uint32_t end, Vec<DT> (&x)[kBatch], Load load) {
+  if (first - (threadIdx.x & 31) + kChunkVectors <= end) {
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) x[k].set(load(at + k * 512));
+  } else {
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (first + k * 32 < end) x[k].set(load(at + k * 512));
+      else x[k].set_empty();
+    }
+  }
+}
+
+// This lane's vectors of a chunk; places past the segment's end are empty.
+// ANY: the body may start anywhere, not on a 16-byte boundary only.
+template <int DT, bool ANY, typename Load>
+__device__ __forceinline__ void load_chunk(const VocabArgs& v, const char* body, const ChunkWalk& w,
+                                           Vec<DT> (&x)[kBatch], Load load) {
+  const uint32_t first = w.vector(), end = w.vectors(v);
+  const char* at = body + static_cast<uint64_t>(first) * 16;
+  if (!ANY || reinterpret_cast<uintptr_t>(body) % 16 == 0) load_vectors<DT>(at, first, end, x, load);
+  else load_vectors<DT>(at, first, end, x, [&](const char* p) { return load_any(p, load); });
+}
 
 // segment of edge element `e` of a row, and its column there
 template <int DT>
@@ -327,14 +389,16 @@ __device__ __forceinline__ void edge_at(const VocabArgs& v, const Segments& s, u
   if (col >= s.head[seg]) col += vectors * Elem<DT>::kVec;
 }
 
-// calls f(x, column) for this thread's elements of vectors [lo, hi) of the
+// calls f(x, column) for this thread's elements of chunks [lo, hi) of the
 // row, one element at a time, and of its edges where `edges` is set
 template <int DT, typename F>
 __device__ void each_element(const VocabArgs& v, const Segments& s, uint32_t lo, uint32_t hi, bool edges, F f) {
   constexpr uint32_t K = Elem<DT>::kVec;
-  for (Walk w(v.cut, lo + threadIdx.x); w.index < hi; w.next(v.cut)) {
-    const uint32_t col = s.head[w.seg] + w.vec * K;
-    for (uint32_t i = 0; i < K; ++i) f(load_one<DT>(s.at<DT>(w.seg, col + i)), w.seg * v.shard + col + i);
+  for (ChunkWalk w(v.cut, lo + (threadIdx.x >> 5)); w.index < hi; w.next(v.cut)) {
+    for (uint32_t k = 0; k < kBatch && w.vector() + k * 32 < w.vectors(v); ++k) {
+      const uint32_t col = s.head[w.seg] + (w.vector() + k * 32) * K;
+      for (uint32_t i = 0; i < K; ++i) f(load_one<DT>(s.at<DT>(w.seg, col + i)), w.seg * v.shard + col + i);
+    }
   }
   for (uint32_t e = threadIdx.x; edges && e < v.cut.edges; e += blockDim.x) {
     uint32_t seg, col;
@@ -399,6 +463,76 @@ __device__ __noinline__ Stats slow_stats(const VocabArgs& v, const Segments& s, 
     }
   }
   return Stats{};
+}
+
+// Adds a chunk's vectors to a thread's part: the largest element first, which
+// it returns, then the sums. s and u are relative to r = a.m c.
+template <int DT, bool ENTROPY>
+__device__ __forceinline__ float add_chunk(Part& a, float& r, f32x2 (&s)[2], f32x2 (&u)[2], Vec<DT> (&x)[kBatch],
+                                           float c) {
+  // distances have to be finite for u only: 2^-inf is 0
+  if (ENTROPY) {
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) x[k].clamp();
+  }
+  const float top = batch_max<DT, kBatch>(x);
+  if (top > a.m) {
+    const float to = __fmul_rn(top, c), d = __fsub_rn(r, to), f = exp2_ftz(d);
+    const f32x2 dd = pack(d, d), ff = pack(f, f);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      // where f is 0, d may be infinite and nothing is left of the sums
+      if (ENTROPY) u[i] = f == 0.f ? 0ull : mul2(ff, fma2(s[i], dd, u[i]));
+      s[i] = f == 0.f ? 0ull : mul2(ff, s[i]);
+    }
+    a.m = top;
+    r = to;
+  }
+  const f32x2 cc = pack(c, c), rr = pack(-r, -r);
+#pragma unroll
+  for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+    for (int i = 0; i < Vec<DT>::kPairs; ++i) {
+      const f32x2 d = fma2(x[k].pair(i), cc, rr);
+      const f32x2 e = exp2x2(d);
+      s[i & 1] = add2(s[i & 1], e);
+      if (ENTROPY) u[i & 1] = fma2(e, d, u[i & 1]);
+    }
+  return top;
+}
+
+// This thread's part of chunks [lo, hi) of the row, and of its edge elements
+// where `edges` is set. `load_vector(address)` loads 16 bytes;
+// `top_of(chunk's maximum)` is called once a chunk.
+template <int DT, bool ENTROPY, bool ANY, typename Load, typename TopF>
+__device__ __forceinline__ Part scan_row(const VocabArgs& v, const Segments& seg, uint32_t lo, uint32_t hi, bool edges,
+                                         Load load_vector, TopF top_of) {
+  const float c = v.exp2_scale;
+  Part a{kClamp, 0.f, 0.f};
+  float r = __fmul_rn(kClamp, c);
+  f32x2 s[2] = {0, 0}, u[2] = {0, 0};
+  for (ChunkWalk w(v.cut, lo + (threadIdx.x >> 5)); w.index < hi; w.next(v.cut)) {
+    Vec<DT> x[kBatch];
+    load_chunk<DT, ANY>(v, seg.at<DT>(w.seg, seg.head[w.seg]), w, x, load_vector);
+    top_of(add_chunk<DT, ENTROPY>(a, r, s, u, x, c));
+  }
+  float s0, s1, s2, s3;
+  unpack(s[0], s0, s1);
+  unpack(s[1], s2, s3);
+  a.s = (s0 + s1) + (s2 + s3);
+  unpack(u[0], s0, s1);
+  unpack(u[1], s2, s3);
+  a.u = (s0 + s1) + (s2 + s3);
+  for (uint32_t e = threadIdx.x; edges && e < v.cut.edges; e += blockDim.x) {
+    uint32_t es, col;
+    edge_at<DT>(v, seg, e, es, col);
+    const float x = max_f32(load_one<DT>(seg.at<DT>(es, col)), kClamp);
+    if (x > a.m) rebase(a, x, c);
+    const float d = __fmaf_rn(x, c, -__fmul_rn(a.m, c)), p = exp2_ftz(d);
+    a.s += p;
+    a.u = __fmaf_rn(p, d, a.u);
+  }
+  return a;
 }
 
 // ---------------------------------------------------------------- teacher
@@ -494,7 +628,7 @@ __device__ __forceinline__ void store_loss(const DistillArgs& a, uint64_t t, con
 // Cuts a row into vectors and edges. `spare`: vectors of a segment given up to
 // the edges at the most, where rows do not start on 16-byte boundaries.
 template <int DT>
-inline void set_cut(VocabArgs& v, int threads, int spare) {
+inline void set_cut(VocabArgs& v, int spare) {
   constexpr uint32_t K = Elem<DT>::kVec;
   const uint32_t last = v.vocab - (v.used - 1) * v.shard;
   const auto vectors = [&](uint32_t n) {
@@ -504,12 +638,17 @@ inline void set_cut(VocabArgs& v, int threads, int spare) {
   VocabCut& c = v.cut;
   c.full = vectors(v.shard);
   c.last = vectors(last);
-  c.divisor = c.full > 0 ? c.full : 1;
-  c.vectors = (v.used - 1) * c.full + c.last;
+  const auto chunks = [](uint32_t n) { return (n + kChunkVectors - 1) / kChunkVectors; };
+  c.per_segment = c.full > 0 ? chunks(c.full) : 1;
+  c.chunks = (v.used - 1) * (c.full > 0 ? c.per_segment : 0) + chunks(c.last);
   c.edge = v.shard - c.full * K;
   c.edges = (v.used - 1) * c.edge + last - c.last * K;
-  c.step_seg = threads / c.divisor;
-  c.step_vec = threads % c.divisor;
+  if (v.used == 1) c.per_segment = c.chunks > 0 ? c.chunks : 1;
+}
+
+inline void set_step(VocabCut& c, int threads) {
+  c.step_seg = threads / 32 / c.per_segment;
+  c.step_part = threads / 32 % c.per_segment;
 }
 
 int launch_distill_forward(int dtype, DistillArgs& a, VocabLaunch& l);
@@ -517,8 +656,9 @@ int launch_distill_forward(int dtype, DistillArgs& a, VocabLaunch& l);
 // Launches `kernel` on clusters of `cluster` CTAs; uncapped calls start early
 // (the kernel waits before it touches memory).
 template <typename Kernel, typename Args>
-inline int launch_rows(Kernel kernel, const Args& a, VocabLaunch& l, uint64_t grid, int threads, int cluster,
+inline int launch_rows(Kernel kernel, Args& a, VocabLaunch& l, uint64_t grid, int threads, int cluster,
                        size_t smem) {
+  set_step(a.v.cut, threads);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
