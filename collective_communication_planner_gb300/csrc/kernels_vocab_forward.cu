@@ -46,16 +46,48 @@ __device__ __forceinline__ uint32_t order_of(float x) {
   const uint32_t b = __float_as_uint(x + 0.f);  // -0 counts as 0
   return (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
+__device__ __forceinline__ float order_value(uint32_t o) {
+  return __uint_as_float((o & 0x80000000u) ? o & 0x7FFFFFFFu : ~o);
+}
 __device__ __forceinline__ uint64_t key_of(float x, uint32_t column) {
   if (!(x > -INFINITY)) return 0;
   return static_cast<uint64_t>(order_of(x)) << 32 | (0xFFFFFFFFu - column);
 }
 __device__ __forceinline__ float key_value(uint64_t k) {
-  const uint32_t o = static_cast<uint32_t>(k >> 32);
-  return __uint_as_float((o & 0x80000000u) ? o & 0x7FFFFFFFu : ~o);
+  return order_value(static_cast<uint32_t>(k >> 32));
 }
 __device__ __forceinline__ int64_t key_column(uint64_t k) {
   return static_cast<int64_t>(0xFFFFFFFFu - static_cast<uint32_t>(k));
+}
+
+// One warp: a value that at least k of the threads' maxima (as orders) reach,
+// and not many more. Bisection: a comparison of all pairs of maxima instead
+// took 1300 instructions a warp, and most of a decode batch's time.
+__device__ __forceinline__ float warp_threshold(const uint32_t* order, int k) {
+  constexpr int N = kThreads / 32;
+  uint32_t mine[N], least = 0xFFFFFFFFu, most = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    mine[i] = order[i * 32 + (threadIdx.x & 31)];
+    least = min(least, mine[i]);
+    most = max(most, mine[i]);
+  }
+  uint32_t lo = __reduce_min_sync(0xFFFFFFFFu, least), hi = __reduce_max_sync(0xFFFFFFFFu, most);
+  // lo is reached by at least k; nothing above hi is reached at all
+  while (lo < hi) {
+    const uint32_t mid = lo + (hi - lo + 1) / 2;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) n += mine[i] >= mid;
+    n = __reduce_add_sync(0xFFFFFFFFu, n);
+    if (n < k) {
+      hi = mid - 1;
+      continue;
+    }
+    lo = mid;
+    if (n <= k + k / 8) break;
+  }
+  return order_value(lo);
 }
 
 struct TopSlots {
@@ -137,9 +169,9 @@ __device__ __noinline__ void select_by_scan(const VocabArgs& v, const Segments& 
 }
 
 // The best k columns among this CTA's chunks [lo, hi) and edge elements,
-// sorted, in t.sorted[0 .. t.found). The k-th largest of the threads' maxima
-// is at most the k-th largest element, so only chunks whose maximum reaches
-// it are read again, by the lanes.
+// sorted, in t.sorted[0 .. t.found). A value that k of the threads' maxima
+// reach is at most the k-th largest element, so only the lanes' shares of
+// chunks whose maximum reaches it are read again.
 template <int DT>
 __device__ void select_top(const VocabArgs& v, const Segments& seg, uint32_t lo, uint32_t hi, bool edges,
                            TopSlots& t, int k, const uint16_t* tops, int shift,
@@ -149,28 +181,21 @@ __device__ void select_top(const VocabArgs& v, const Segments& seg, uint32_t lo,
     select_by_scan<DT>(v, seg, lo, hi, edges, t, k);
     return;
   }
-  const uint32_t mine = order_of(thread_max);
-  t.order[threadIdx.x] = mine;
+  t.order[threadIdx.x] = order_of(thread_max);
   if (threadIdx.x == 0) t.candidates = t.works = 0;
   __syncthreads();
-  int place = 0;
-  const uint4* all = reinterpret_cast<const uint4*>(t.order);
-#pragma unroll 4
-  for (int i = 0; i < kThreads / 4; ++i) {
-    const uint4 o = all[i];
-    const int j = 4 * i, me = threadIdx.x;
-    place += (o.x > mine || (o.x == mine && j < me)) + (o.y > mine || (o.y == mine && j + 1 < me)) +
-             (o.z > mine || (o.z == mine && j + 2 < me)) + (o.w > mine || (o.w == mine && j + 3 < me));
+  if (threadIdx.x < 32) {
+    const float found = warp_threshold(t.order, k);
+    if (threadIdx.x == 0) t.threshold = found;
   }
-  if (place == k - 1) t.threshold = thread_max;
   __syncthreads();
-  // at the clamp: too few threads have an element above it, any element counts
-  const float threshold = t.threshold > kClamp ? t.threshold : -INFINITY;
+  const float threshold = t.threshold;
+  const auto reaches = [&](float x) { return x >= threshold && x > kClamp; };
   const int warps = kThreads / 32, warp = threadIdx.x / 32;
   const int chunks = lo + warp < hi ? (hi - lo - warp + warps - 1) / warps : 0;
   const int entries = (chunks + (1 << shift) - 1) >> shift;
   for (int i = 0; i < entries; ++i) {
-    if (__uint_as_float(static_cast<uint32_t>(tops[i * kThreads + threadIdx.x]) << 16) >= threshold) {
+    if (reaches(__uint_as_float(static_cast<uint32_t>(tops[i * kThreads + threadIdx.x]) << 16))) {
       const int n = atomicAdd(&t.works, 1);
       if (n < kMaxWork) t.work[n] = i * kThreads + threadIdx.x;
     }
@@ -179,7 +204,7 @@ __device__ void select_top(const VocabArgs& v, const Segments& seg, uint32_t lo,
     uint32_t es, col;
     edge_at<DT>(v, seg, e, es, col);
     const float x = load_one<DT>(seg.at<DT>(es, col));
-    if (x >= threshold) offer(t, x, es * v.shard + col);
+    if (reaches(x)) offer(t, x, es * v.shard + col);
   }
   __syncthreads();
   if (t.works <= kMaxWork) {
@@ -196,13 +221,20 @@ __device__ void select_top(const VocabArgs& v, const Segments& seg, uint32_t lo,
       x.set(dev::ld_global_v4(seg.at<DT>(w.seg, col)));
 #pragma unroll
       for (int j = 0; j < K; ++j)
-        if (x.get(j) >= threshold) offer(t, x.get(j), w.seg * v.shard + col + j);
+        if (reaches(x.get(j))) offer(t, x.get(j), w.seg * v.shard + col + j);
     }
   }
   __syncthreads();
   const int n = t.candidates;
-  if (t.works <= kMaxWork && n <= kMaxCandidates) sort_candidates(t, n, k);
-  else select_by_scan<DT>(v, seg, lo, hi, edges, t, k);
+  bool whole = t.works > kMaxWork || n > kMaxCandidates;
+  if (!whole && n < k) {
+    // fewer than k columns above the clamp: there may be some below it
+    bool below = false;
+    each_element<DT>(v, seg, lo, hi, edges, [&](float x) { below = below || (x <= kClamp && x > -INFINITY); });
+    whole = __syncthreads_or(below);
+  }
+  if (whole) select_by_scan<DT>(v, seg, lo, hi, edges, t, k);
+  else sort_candidates(t, n, k);
 }
 
 struct ClusterTop {
@@ -252,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 5) log_probs_kernel(const __grid_con
     float* out_lp = a.top_log_probs + t * k;
     int64_t* out_id = a.top_ids + t * k;
     int found = 0;
-    if (scored && !st.bad()) {
+    if (scored && !st.bad() && !st.empty()) {
       select_top<DT>(v, seg, lo, hi, cta == 0, *top, k, tops, a.entry_shift, thread_max,
                      !(fabsf(st.max) < -kClamp));
       const int mine = top->found;

@@ -8,7 +8,7 @@ namespace {
 using namespace vocab;
 
 constexpr int kThreads = 256;
-constexpr uint64_t kKeepBytes = 40ull << 20;  // rows that L2 keeps between two reads
+constexpr uint64_t kKeepBytes = 52ull << 20;  // rows that L2 keeps between two reads
 
 // The segments of the current row for a gradient: where the logits and the
 // gradient start, and the first element of the body, which starts on a 16-byte
@@ -303,12 +303,13 @@ __global__ void __launch_bounds__(kThreads, 5) distill_grad_kernel(const __grid_
 }
 
 constexpr int kStepCluster = 8;
+constexpr int kStepCtasPerSm = 5;
 
 // Loss and gradient in one call: a cluster of CTAs sums up a row, joins its
 // statistics through distributed shared memory and reads it again, from L2,
 // for the gradient.
 template <int DT>
-__global__ void __launch_bounds__(kThreads, 5) distill_step_kernel(const __grid_constant__ DistillArgs a) {
+__global__ void __launch_bounds__(kThreads, kStepCtasPerSm) distill_step_kernel(const __grid_constant__ DistillArgs a) {
   __shared__ GradSegments seg;
   __shared__ Named named;
   __shared__ LossSlots loss;
@@ -375,11 +376,11 @@ int launch_step_t(DistillArgs& a, VocabLaunch& l) {
   // CTAs of a row: few enough rows at once for L2 to keep them between the two
   // reads, or as many as the SMs take of few rows; every warp gets a chunk
   const uint64_t row_bytes = static_cast<uint64_t>(v.vocab) * Elem<DT>::kBytes;
-  const uint64_t resident = static_cast<uint64_t>(l.sm_count) * 4;
+  const uint64_t resident = static_cast<uint64_t>(l.sm_count) * kStepCtasPerSm;
+  const auto kept = [&](int c) { return (v.rows < resident / c ? v.rows : resident / c) * row_bytes; };
   int c = 1;
   while (c < kStepCluster && v.cut.chunks >= static_cast<uint32_t>(2 * c * kThreads / 32) &&
-         (l.cap <= 0 || 2 * c <= l.cap) &&
-         (v.rows * 2 * c <= resident || (v.rows * c > resident && resident / c * row_bytes > kKeepBytes)))
+         (l.cap <= 0 || 2 * c <= l.cap) && (v.rows * 2 * c <= resident || kept(c) > kKeepBytes))
     c *= 2;
   uint64_t rows = v.rows;
   if (l.cap > 0 && rows * c > static_cast<uint64_t>(l.cap)) rows = l.cap / c;

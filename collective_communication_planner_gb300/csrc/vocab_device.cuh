@@ -389,21 +389,24 @@ __device__ __forceinline__ void edge_at(const VocabArgs& v, const Segments& s, u
   if (col >= s.head[seg]) col += vectors * Elem<DT>::kVec;
 }
 
-// calls f(x, column) for this thread's elements of chunks [lo, hi) of the
-// row, one element at a time, and of its edges where `edges` is set
+// calls f(x) for this thread's elements of chunks [lo, hi) of the row, and of
+// its edges where `edges` is set
 template <int DT, typename F>
-__device__ void each_element(const VocabArgs& v, const Segments& s, uint32_t lo, uint32_t hi, bool edges, F f) {
-  constexpr uint32_t K = Elem<DT>::kVec;
+__device__ __forceinline__ void each_element(const VocabArgs& v, const Segments& s, uint32_t lo, uint32_t hi,
+                                             bool edges, F f) {
   for (ChunkWalk w(v.cut, lo + (threadIdx.x >> 5)); w.index < hi; w.next(v.cut)) {
-    for (uint32_t k = 0; k < kBatch && w.vector() + k * 32 < w.vectors(v); ++k) {
-      const uint32_t col = s.head[w.seg] + (w.vector() + k * 32) * K;
-      for (uint32_t i = 0; i < K; ++i) f(load_one<DT>(s.at<DT>(w.seg, col + i)), w.seg * v.shard + col + i);
-    }
+    Vec<DT> x[kBatch];
+    load_chunk<DT, true>(v, s.at<DT>(w.seg, s.head[w.seg]), w, x, StreamLoad());
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      if (w.vector() + k * 32 < w.vectors(v))
+#pragma unroll
+        for (int i = 0; i < Elem<DT>::kVec; ++i) f(x[k].get(i));
   }
   for (uint32_t e = threadIdx.x; edges && e < v.cut.edges; e += blockDim.x) {
     uint32_t seg, col;
     edge_at<DT>(v, s, e, seg, col);
-    f(load_one<DT>(s.at<DT>(seg, col)), seg * v.shard + col);
+    f(load_one<DT>(s.at<DT>(seg, col)));
   }
 }
 
@@ -414,14 +417,14 @@ template <int DT>
 __device__ __noinline__ Stats slow_stats(const VocabArgs& v, const Segments& s, uint32_t lo, uint32_t hi,
                                          JoinSlots& slots, int& phase, uint32_t cta, uint32_t ctas) {
   float m = -INFINITY;
-  each_element<DT>(v, s, lo, hi, cta == 0, [&](float x, uint32_t) { m = fmaxf(m, x); });
+  each_element<DT>(v, s, lo, hi, cta == 0, [&](float x) { m = fmaxf(m, x); });
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   // max and sum joined apart, in the slots of two joins
   for (int round = 0; round < 2; ++round) {
     float p = m, q = 0.f;  // round 0: the maximum; round 1: s and u
     if (round == 1) {
       p = 0.f;
-      each_element<DT>(v, s, lo, hi, cta == 0, [&](float x, uint32_t) {
+      each_element<DT>(v, s, lo, hi, cta == 0, [&](float x) {
         if (x == -INFINITY) return;
         const float d = (x - m) * v.exp2_scale, e = exp2_ftz(d);
         p += e;
