@@ -23,7 +23,8 @@ HOST_SOURCES = ["api.cpp", "plan.cpp", "reshard.cpp", "copy_out_host.cpp",
 CUDA_SOURCES = ["kernels_bulk.cu", "kernels_small_ar.cu", "kernels_small_rs.cu",
                 "kernels_small_ag.cu", "kernels_reshard.cu", "kernels_rmsnorm.cu",
                 "no_alloc.cu", "kernels_copy_out.cu", "kernels_vocab_forward.cu",
-                "kernels_vocab_grad.cu"]
+                "kernels_vocab_grad.cu", "kernels_vocab_step.cu",
+                "kernels_vocab_ring.cu"]
 
 
 def _cuda_home() -> Path:

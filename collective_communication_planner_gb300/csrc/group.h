@@ -13,6 +13,7 @@
 #include "plan.h"
 #include "reshard.h"
 #include "tccl.h"
+#include "vocab.h"
 
 namespace tccl {
 
@@ -87,6 +88,8 @@ struct tcclGroup {
   uint64_t inject_ns = 0;
   std::map<tccl::PlanKey, std::unique_ptr<tccl::CachedPlan>> plans;
   std::map<std::string, std::unique_ptr<tccl::CachedReshard>> reshards;
+  // distillation ring: clusters of each size that fit on the device at once
+  int ring_clusters[2 * (tccl::kRingMaxCluster + 1)] = {};
   tcclLaunchInfo_t last;
   // copy-out engine: the group's own copy streams and the events that order
   // them after each segment's kernel and join them back to the caller

@@ -150,7 +150,7 @@ __device__ __noinline__ void select_by_scan(const VocabArgs& v, const Segments& 
   };
   __syncthreads();
   ChunkWalk w(v.cut, lo + threadIdx.x / 32);
-  for (uint32_t i = lo; i < hi; i += kThreads / 32, w.next(v.cut)) {
+  for (uint32_t i = lo; i < hi; i += kThreads / 32, w.next(v.cut, v.step)) {
     for (int k = 0; k < kBatch; ++k) {
       const bool on = w.index < hi && w.vector() + k * 32 < w.vectors(v);
       const uint32_t col = on ? seg.head[w.seg] + (w.vector() + k * 32) * K : 0;
@@ -349,7 +349,12 @@ __global__ void __launch_bounds__(kThreads, 5) distill_kernel(const __grid_const
     set_segments<DT>(v, t, seg);
     __syncthreads();
     const bool mine = cta == 0 && threadIdx.x < 32;
-    if (mine) set_loss<DT>(v, seg, read_teacher(a, t), loss);
+    if (mine) {
+      const TeacherRow q = read_teacher(a, t);
+      uint32_t x[kMaxTop / 32];
+      load_named<DT>(v, t, q, x);
+      set_loss<DT>(q, x, loss);
+    }
     float unused;
     const Stats st = row_stats<DT, false, false>(v, seg, lo, hi, cta, ctas, slots, phase, nullptr, 0, unused);
     if (mine) store_loss(a, t, loss, st);
@@ -406,10 +411,9 @@ int launch_log_probs(int dtype, LogProbsArgs& a, VocabLaunch& l) {
   return a.top_k ? launch_log_probs_t<kF32, true>(a, l) : launch_log_probs_t<kF32, false>(a, l);
 }
 
-namespace vocab {
-int launch_distill_forward(int dtype, DistillArgs& a, VocabLaunch& l) {
+int launch_distill(int dtype, DistillArgs& a, VocabLaunch& l) {
+  if (a.weights) return vocab::launch_distill_step(dtype, a, l);
   return dtype == kBF16 ? launch_distill_t<kBF16>(a, l) : launch_distill_t<kF32>(a, l);
 }
-}  // namespace vocab
 
 }  // namespace tccl

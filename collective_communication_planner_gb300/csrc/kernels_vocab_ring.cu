@@ -1,0 +1,581 @@
+// Distillation with its gradient on long rows: a persistent, warp-specialised
+// ring, so that a logit is read from memory once.
+//
+// A cluster of CTAs, one to an SM, takes rows in turn; each CTA has a slice of
+// the row in a shared-memory slot, which the loader warp fills with bulk copies,
+// until its gradient is written. The sum warps take a row's slice first, and
+// each sends its part to every CTA of the cluster (distributed shared memory and
+// one mbarrier arrival each). The gradient warps, rows behind the sum warps,
+// write the gradient when a row's parts are in. Three teacher warps take the rows in turn: they read the teacher's
+// entries three rows ahead, give the named columns their own term after the
+// gradient, and do the row's few edge elements and its loss.
+//
+// Every wait is bounded; on expiry a warp records the timeout in the group's
+// status word and sets the CTA's abort flag, its CTA's other warps give up too,
+// the loader waits for its copies in flight, and all warps of the cluster meet
+// at its last barrier, so that no CTA writes to one that has left.
+#include "vocab_grad.cuh"
+
+namespace tccl {
+namespace {
+
+using namespace vocab;
+
+constexpr uint32_t kSumWarps = 12, kGradWarps = 12;
+constexpr uint32_t kTeacherWarps = 3;  // they take the rows in turn
+constexpr uint32_t kLoaderWarp = kSumWarps + kGradWarps, kFirstTeacher = kLoaderWarp + 1;
+constexpr int kThreads = (kFirstTeacher + kTeacherWarps) * 32;
+constexpr uint32_t kMinChunks = 16;  // a CTA's slice: 32 KiB
+constexpr int kMinSlots = 3, kMaxSlots = 4;
+// What goes with a row within the CTA, row n's being set n % kSets. A teacher
+// warp sets row n + 3's up before it is done with row n, and row n + 6's after
+// that: every warp that reads row n's set is past it then.
+constexpr uint32_t kSets = 2 * kTeacherWarps;
+// The parts of a row, row n's being set n % kJoins: from every CTA of the
+// cluster the sum warps' and, as the last, the edge elements' from the row's
+// teacher warp. A warp of another CTA sends row n only when all have sent row
+// n - kMaxSlots (a slot is free only then) and its teacher n - kTeacherWarps;
+// this CTA's gradient warps have then read the parts up to row n - 2 kMaxSlots,
+// and its teacher warps up to row n - kMaxSlots - kTeacherWarps.
+constexpr uint32_t kParts = kSumWarps + 1;
+constexpr uint32_t kJoins = 9;
+static_assert(kJoins > 2 * kMaxSlots && kJoins > kMaxSlots + kTeacherWarps, "parts overwritten while they may be read");
+
+struct RingShared {
+  uint64_t full[kMaxSlots];   // a slot's copies have landed (bytes)
+  uint64_t empty[kMaxSlots];  // every gradient warp is done with a slot's row
+  uint64_t done[kSets];       // every gradient warp has written its share of a row
+  uint64_t joined[kJoins];    // every part of a row is in `part`: this CTA's sum warps' and all
+                              // teacher warps' arrivals, the other sum warps' bytes
+  uint64_t never;             // test hook
+  float2 part[kJoins][kRingMaxCluster * kParts];  // maximum and sum
+  GradSegments seg[kMaxSlots], edge_seg[kTeacherWarps];
+  Named named[kSets];
+  LossSlots loss[kSets];
+  float weight[kSets];
+  int abort;
+};
+constexpr size_t kSharedBytes = (sizeof(RingShared) + 127) / 128 * 128;
+
+// arrives at `bar` of CTA `rank` of the cluster, after this thread's remote stores
+__device__ __forceinline__ void remote_arrive(const uint64_t* bar, uint32_t rank) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote(bar, rank)) : "memory");
+}
+
+__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(dev::smem_addr(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
+// A warp's bounded wait for the phase of use number `use` of a barrier; false
+// in every lane if any gave up, or if another warp of the CTA has.
+struct Wait {
+  volatile int* abort;
+  int* status;
+  uint64_t timeout_ns;
+  __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t use, bool honour_abort = true) const {
+    bool ok = try_wait_cluster(bar, use & 1);
+    if (!__all_sync(0xFFFFFFFFu, ok)) ok = slow(bar, use & 1, honour_abort);
+    return __all_sync(0xFFFFFFFFu, ok);
+  }
+  __device__ __noinline__ bool slow(uint64_t* bar, uint32_t parity, bool honour_abort) const {
+    const uint64_t t0 = dev::global_ns();
+    for (uint32_t i = 1;; ++i) {
+      if (try_wait_cluster(bar, parity)) return true;
+      if (honour_abort && *abort) return false;
+      if ((i & 31) == 0 && dev::global_ns() - t0 > timeout_ns) {
+        *abort = 1;
+        atomicCAS(status, 0, kStatusTimeout);
+        return false;
+      }
+    }
+  }
+};
+
+// As rebase and lanes_join, for any maxima: the distance is taken before the
+// product, which an infinite or a huge maximum would turn into NaN.
+__device__ __forceinline__ Part join_lanes_any(Part a, float c) {
+  float m = a.m;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  if (a.m != m) a.s *= exp2_ftz((a.m - m) * c);
+  a.m = m;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) a.s += __shfl_xor_sync(0xFFFFFFFFu, a.s, o);
+  return a;
+}
+
+__device__ __forceinline__ Stats stats_any(const Part& a) {
+  Stats r;
+  r.max = a.m;
+  r.log2_s = a.m == -INFINITY && a.s == 0.f ? 0.f : log2f(a.s);
+  r.entropy = 0.f;
+  return r;
+}
+
+struct SharedLoad {
+  __device__ __forceinline__ uint4 operator()(const char* at) const { return *reinterpret_cast<const uint4*>(at); }
+};
+
+// Where a chunk is in its slot: one chunk behind the other, and sixteen bytes
+// more for each segment before it, whose logits may reach into one more granule
+// than they are long.
+__device__ __forceinline__ const char* slot_chunk(const char* slot, const ChunkWalk& w, uint32_t lo, uint32_t seg0) {
+  return slot + (w.index - lo) * (kChunkVectors * 16) + (w.seg - seg0) * 16;
+}
+
+// A lane's vectors of a chunk in its slot. `m`: how far the logits are from
+// the 16-byte granules that were copied.
+template <int DT>
+__device__ __forceinline__ void load_slot(const char* chunk, uint32_t m, const ChunkWalk& w, uint32_t end,
+                                          Vec<DT> (&x)[kBatch]) {
+  const char* at = chunk + (threadIdx.x & 31) * 16;
+  if (m == 0) load_vectors<DT>(at, w.vector(), end, x, SharedLoad());
+  else load_vectors<DT>(at + m, w.vector(), end, x, [](const char* p) { return load_any(p, SharedLoad()); });
+}
+
+// how far the logits of a segment's body are from a 16-byte boundary
+template <int DT>
+__device__ __forceinline__ uint32_t off_granule(const GradSegments& s, uint32_t seg) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(s.at<DT>(seg, s.head[seg])) & 15);
+}
+
+// A warp's part of the slice in a slot.
+template <int DT>
+__device__ __forceinline__ Part slot_part(const VocabArgs& v, const GradSegments& s, const char* slot,
+                                          uint32_t lo, uint32_t hi, uint32_t warp, const ChunkStep& step) {
+  const float c = v.exp2_scale;
+  const uint32_t seg0 = lo / v.cut.per_segment;
+  Part p{-INFINITY, 0.f, 0.f};
+  f32x2 sum[4] = {0, 0, 0, 0};
+  for (ChunkWalk w(v.cut, lo + warp); w.index < hi; w.next(v.cut, step)) {
+    Vec<DT> x[kBatch];
+    load_slot<DT>(slot_chunk(slot, w, lo, seg0), off_granule<DT>(s, w.seg), w, w.vectors(v), x);
+    const float top = fmaxf(p.m, batch_max<DT, kBatch>(x));
+    // a first maximum finds sums of 0; the same maximum, -inf among them, changes nothing
+    const float f = top == p.m ? 1.f : exp2_ftz((p.m - top) * c);
+    p.m = top;
+    const float from = top == -INFINITY ? 0.f : top;  // -inf so far: the terms are 0, not NaN
+    const f32x2 ff = pack(f, f), mm = pack(-from, -from), cc = pack(c, c);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum[i] = mul2(sum[i], ff);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+      for (int i = 0; i < Vec<DT>::kPairs; ++i)
+        sum[i % 4] = add2(sum[i % 4], exp2x2(mul2(add2(x[k].pair(i), mm), cc)));
+  }
+  float s0, s1, s2, s3;
+  unpack(add2(sum[0], sum[1]), s0, s1);
+  unpack(add2(sum[2], sum[3]), s2, s3);
+  p.s = (s0 + s1) + (s2 + s3);
+  return p;
+}
+
+// The gradient of a warp's chunks of the slice in a slot.
+template <int DT, bool FAST>
+__device__ __forceinline__ void store_slot(const VocabArgs& v, const GradSegments& s, const RowGrad& g,
+                                           const char* slot, uint32_t lo, uint32_t hi, uint32_t warp, const ChunkStep& step) {
+  const uint32_t seg0 = lo / v.cut.per_segment;
+  for (ChunkWalk w(v.cut, lo + warp); w.index < hi; w.next(v.cut, step)) {
+    Vec<DT> x[kBatch];
+    const uint32_t first = w.vector(), end = w.vectors(v);
+    load_slot<DT>(slot_chunk(slot, w, lo, seg0), off_granule<DT>(s, w.seg), w, end, x);
+    store_chunk<DT, false, FAST>(g, x, s.to<DT>(w.seg, s.head[w.seg]) + static_cast<uint64_t>(first) * 16, first, end);
+  }
+}
+
+// The rows a cluster takes: row(n) = first + n step, n < count.
+struct Rows {
+  uint64_t first, step;
+  uint32_t count;
+  __device__ __forceinline__ uint64_t row(uint32_t n) const { return first + n * step; }
+};
+
+// Sends a sum warp's part of row n, the same in every lane, to every CTA of the
+// cluster. To another CTA: an asynchronous store whose bytes count towards its
+// barrier (a store and a releasing arrival instead waited 1.5 to 2 us behind the
+// gradient warps' stores). To its own, a store and an arrival.
+__device__ __forceinline__ void send_part(RingShared& s, uint32_t n, uint32_t cta, uint32_t ctas, uint32_t warp,
+                                          const Part& p) {
+  const uint32_t lane = threadIdx.x & 31;
+  if (lane >= ctas) return;
+  float2* part = &s.part[n % kJoins][cta * kParts + warp];
+  uint64_t* joined = &s.joined[n % kJoins];
+  if (lane == cta) {
+    *part = make_float2(p.m, p.s);
+    dev::mbar_arrive(joined);
+  } else {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(
+                     remote(part, lane)),
+                 "f"(p.m), "f"(p.s), "r"(remote(joined, lane))
+                 : "memory");
+  }
+}
+
+// The same for the edge elements' part, by the row's teacher warp: its arrivals
+// release what the warp has written (to its CTA) and read (to the others, which
+// may replace it). The one at the CTA's own barrier says how many bytes the
+// other CTAs' sum warps send.
+__device__ __forceinline__ void send_last_part(RingShared& s, uint32_t n, uint32_t cta, uint32_t ctas, const Part& p) {
+  const uint32_t lane = threadIdx.x & 31;
+  if (lane >= ctas) return;
+  float2* part = &s.part[n % kJoins][cta * kParts + kSumWarps];
+  uint64_t* joined = &s.joined[n % kJoins];
+  if (lane == cta) {
+    *part = make_float2(p.m, p.s);
+    dev::mbar_arrive_expect_tx(joined, (ctas - 1) * kSumWarps * 8);
+  } else {
+    const uint32_t at = remote(part, lane);
+    remote_store(at, p.m);
+    remote_store(at + 4, p.s);
+    remote_arrive(joined, lane);
+  }
+}
+
+// the statistics of row n from all its parts; every lane of the warp
+__device__ __forceinline__ Stats row_parts(const RingShared& s, uint32_t n, uint32_t ctas, float c) {
+  Part p{-INFINITY, 0.f, 0.f};
+  for (uint32_t i = threadIdx.x & 31; i < ctas * kParts; i += 32) {
+    const float2 o = s.part[n % kJoins][i];
+    const float m = fmaxf(p.m, o.x);
+    // equal maxima, -inf among them, leave a sum as it is
+    p.s = (p.m == m ? p.s : p.s * exp2_ftz((p.m - m) * c)) + (o.x == m ? o.y : o.y * exp2_ftz((o.x - m) * c));
+    p.m = m;
+  }
+  return stats_any(join_lanes_any(p, c));
+}
+
+template <int DT>
+__device__ void sum_warp(const DistillArgs& a, RingShared& s, const unsigned char* ring, const Rows& rows,
+                         uint32_t cta, uint32_t ctas, uint32_t lo, uint32_t hi, const Wait& wait) {
+  const uint32_t warp = threadIdx.x >> 5;
+  for (uint32_t n = 0; n < rows.count; ++n) {
+    const uint32_t slot = n % a.slots;
+    if (!wait(&s.full[slot], n / a.slots)) return;
+    const char* at = reinterpret_cast<const char*>(ring) + static_cast<size_t>(slot) * a.slot_bytes;
+    const Part p = slot_part<DT>(a.v, s.seg[slot], at, lo, hi, warp, a.sum_step);
+    send_part(s, n, cta, ctas, warp, join_lanes_any(p, a.v.exp2_scale));
+  }
+}
+
+template <int DT>
+__device__ void grad_warp(const DistillArgs& a, RingShared& s, const unsigned char* ring, const Rows& rows,
+                          uint32_t cta, uint32_t ctas, uint32_t lo, uint32_t hi, const Wait& wait) {
+  const VocabArgs& v = a.v;
+  const uint32_t warp = (threadIdx.x >> 5) - kSumWarps;
+  for (uint32_t n = 0; n < rows.count; ++n) {
+    const uint32_t slot = n % a.slots;
+    if (!wait(&s.joined[n % kJoins], n / kJoins)) return;
+    if (!wait(&s.full[slot], n / a.slots)) return;  // long done; makes the copies visible to this warp
+    const Stats st = row_parts(s, n, ctas, v.exp2_scale);
+    const float w = s.weight[n % kSets], total = s.named[n % kSets].total;
+    const GradSegments& seg = s.seg[slot];
+    if (w == 0.f || total == 0.f || st.empty()) {
+      zero_chunks<DT>(v, seg, lo, hi, warp, a.grad_step);
+    } else {
+      RowGrad g;
+      g.set(v, st.max, st.log2_s, w * total, 0.f);
+      const char* at = reinterpret_cast<const char*>(ring) + static_cast<size_t>(slot) * a.slot_bytes;
+      if (g.fast) store_slot<DT, true>(v, seg, g, at, lo, hi, warp, a.grad_step);
+      else store_slot<DT, false>(v, seg, g, at, lo, hi, warp, a.grad_step);
+    }
+    zero_padding<DT>(v, rows.row(n), cta * kGradWarps * 32 + threadIdx.x - kSumWarps * 32, ctas * kGradWarps * 32);
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) {
+      dev::mbar_arrive(&s.empty[slot]);
+      dev::mbar_arrive(&s.done[n % kSets]);
+    }
+  }
+}
+
+// A lane's share of what the loader copies of every row: pieces of segments
+// first + lane, first + lane + 32 of the slice.
+struct Piece {
+  uint32_t seg, begin, vectors, to;  // vectors [begin, begin + vectors) of the segment, at byte `to` of a slot
+};
+
+// Starts the copies of row n's slice into its slot, one a segment (a copy a
+// chunk, 32 of 2 KiB, took the warp 2 us to issue).
+template <int DT>
+__device__ __forceinline__ void fill_slot(const DistillArgs& a, RingShared& s, unsigned char* ring, const Rows& rows,
+                                          uint32_t n, const Piece (&piece)[kMaxRanks / 32]) {
+  const VocabArgs& v = a.v;
+  const uint32_t slot = n % a.slots, lane = threadIdx.x & 31;
+  GradSegments& seg = s.seg[slot];
+  for (uint32_t r = lane; r < v.used; r += 32) set_segment<DT>(v, rows.row(n), r, seg);
+  __syncwarp();
+  uint32_t total = 0, bytes[kMaxRanks / 32];
+  const char* from[kMaxRanks / 32];
+#pragma unroll
+  for (int i = 0; i < kMaxRanks / 32; ++i) {
+    const Piece& p = piece[i];
+    bytes[i] = 0;
+    if (p.vectors == 0) continue;
+    const uint32_t off = off_granule<DT>(seg, p.seg);
+    bytes[i] = (p.vectors + (off ? 1 : 0)) * 16;  // whole granules
+    from[i] = seg.at<DT>(p.seg, seg.head[p.seg]) - off + static_cast<uint64_t>(p.begin) * 16;
+    total += bytes[i];
+  }
+  total = __reduce_add_sync(0xFFFFFFFFu, total);
+  if (lane == 0) dev::mbar_arrive_expect_tx(&s.full[slot], total);
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < kMaxRanks / 32; ++i)
+    if (bytes[i])
+      dev::bulk_load(ring + static_cast<size_t>(slot) * a.slot_bytes + piece[i].to, from[i], bytes[i], &s.full[slot]);
+}
+
+template <int DT>
+__device__ void loader_warp(const DistillArgs& a, RingShared& s, unsigned char* ring, const Rows& rows, uint32_t lo,
+                            uint32_t hi, const Wait& wait) {
+  const VocabCut& c = a.v.cut;
+  const uint32_t lane = threadIdx.x & 31, slots = a.slots, seg0 = lo / c.per_segment;
+  Piece piece[kMaxRanks / 32];
+#pragma unroll
+  for (uint32_t i = 0; i < kMaxRanks / 32; ++i) {
+    Piece& p = piece[i];
+    p.seg = seg0 + lane + 32 * i;
+    p.vectors = 0;
+    const uint32_t from = p.seg * c.per_segment, all = p.seg + 1 == a.v.used ? c.last : c.full;
+    if (lo >= hi || p.seg >= a.v.used || from >= hi) continue;
+    p.begin = lo > from ? (lo - from) * kChunkVectors : 0;
+    p.vectors = min(all, (hi - from) * kChunkVectors) - p.begin;
+    p.to = lo > from ? 0 : (from - lo) * (kChunkVectors * 16) + (p.seg - seg0) * 16;
+  }
+  uint32_t n = 0;
+  for (; n < rows.count && n < slots; ++n) fill_slot<DT>(a, s, ring, rows, n, piece);
+  bool ok = true;
+  if (a.inject_timeout_ns && blockIdx.x == 0) {
+    Wait hook = wait;
+    hook.timeout_ns = a.inject_timeout_ns;
+    ok = hook(&s.never, 0);
+  }
+  for (; ok && n < rows.count; ++n) {
+    ok = wait(&s.empty[n % slots], n / slots - 1);
+    if (ok) fill_slot<DT>(a, s, ring, rows, n, piece);
+    else break;
+  }
+  // where all went well the sum warps wait for every copy; where another warp
+  // has given up they may not
+  if (ok && n == rows.count) {
+    for (uint32_t r = n > slots ? n - slots : 0; ok && r < n; ++r) ok = wait(&s.full[r % slots], r / slots);
+    if (ok) return;
+  }
+  for (uint32_t r = n > slots ? n - slots : 0; r < n; ++r) wait(&s.full[r % slots], r / slots, false);
+}
+
+template <int DT>
+__device__ void teacher_warp(const DistillArgs& a, RingShared& s, const Rows& rows, uint32_t cta, uint32_t ctas,
+                             uint32_t lo, uint32_t hi, const Wait& wait) {
+  const VocabArgs& v = a.v;
+  const float c = v.exp2_scale;
+  const uint32_t lane = threadIdx.x & 31, mine = (threadIdx.x >> 5) - kFirstTeacher;
+  GradSegments& edge_seg = s.edge_seg[mine];
+  const auto set_edges = [&](uint64_t t) {
+    __syncwarp();
+    for (uint32_t r = lane; r < v.used; r += 32) set_segment<DT>(v, t, r, edge_seg);
+    __syncwarp();
+  };
+  // A row's loads are issued an iteration (three rows) before they are used:
+  // its entries, then the logits at their columns. `entries` and `weight` are the
+  // next row's to be begun, q and x the one's begun.
+  TeacherEntries entries;
+  TeacherRow q;
+  uint32_t x[kMaxTop / 32];
+  float weight = 0.f, next_weight = 0.f;
+  const auto load = [&](uint32_t n) {
+    if (n >= rows.count) return;
+    entries = load_teacher(a, rows.row(n));
+    next_weight = a.weights[rows.row(n)];
+  };
+  const auto begin = [&](uint32_t n) {
+    if (n >= rows.count) return;
+    q = teacher_row(a, entries);
+    weight = next_weight * v.inv_temp;
+    load_named<DT>(v, rows.row(n), q, x);
+  };
+  // The row's set is complete and, with the edge elements' part as the last of
+  // the row's parts, the row may go to the other CTAs: all that they replace of
+  // it, in place, has been read.
+  const auto finish = [&](uint32_t n) {
+    if (n >= rows.count) return;
+    const uint64_t t = rows.row(n);
+    keep_named<DT>(v, t, q, x, a.top_k, s.named[n % kSets], lo, hi, cta == 0);
+    Part p{-INFINITY, 0.f, 0.f};
+    if (cta == 0) {
+      set_loss<DT>(q, x, s.loss[n % kSets]);
+      if (v.cut.edges) set_edges(t);
+      for (uint32_t e = lane; e < v.cut.edges; e += 32) {
+        uint32_t seg, col;
+        edge_at<DT>(v, edge_seg, e, seg, col);
+        const float y = load_one<DT>(edge_seg.at<DT>(seg, col));
+        if (y > p.m) {
+          p.s *= exp2_ftz((p.m - y) * c);
+          p.m = y;
+        }
+        if (y != -INFINITY) p.s += exp2_ftz((y - (p.m == -INFINITY ? 0.f : p.m)) * c);
+      }
+    }
+    p = join_lanes_any(p, c);
+    if (lane == 0) s.weight[n % kSets] = weight;
+    __syncwarp();  // the set, for the release in the arrival at this CTA's barrier
+    send_last_part(s, n, cta, ctas, p);
+  };
+  load(mine);
+  begin(mine);
+  load(mine + kTeacherWarps);
+  finish(mine);
+  for (uint32_t n = mine; n < rows.count; n += kTeacherWarps) {
+    const uint64_t t = rows.row(n);
+    begin(n + kTeacherWarps);
+    load(n + 2 * kTeacherWarps);
+    if (!wait(&s.joined[n % kJoins], n / kJoins)) return;
+    const Stats st = row_parts(s, n, ctas, c);
+    const Named& named = s.named[n % kSets];
+    const float w = s.weight[n % kSets];
+    RowGrad g;
+    g.set(v, st.max, st.log2_s, w * named.total, 0.f);
+    g.zero = w == 0.f || named.total == 0.f || st.empty();
+    if (cta == 0) {
+      store_loss(a, t, s.loss[n % kSets], st);
+      if (v.cut.edges) set_edges(t);
+      for (uint32_t e = lane; e < v.cut.edges; e += 32) {
+        uint32_t seg, col;
+        edge_at<DT>(v, edge_seg, e, seg, col);
+        store_one<DT>(edge_seg.to<DT>(seg, col), g.zero ? 0.f : g.one(load_one<DT>(edge_seg.at<DT>(seg, col))));
+      }
+    }
+    finish(n + kTeacherWarps);
+    // behind the body's stores (the gradient warps') and the edges' (this warp's)
+    if (!wait(&s.done[n % kSets], n / kSets)) return;
+    __syncwarp();
+    if (!g.zero)
+      for (int i = lane; i < named.count; i += 32) store_named<DT>(v, t, named, g, w, i);
+    __syncwarp();
+  }
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kThreads, 1) distill_ring_kernel(const __grid_constant__ DistillArgs a) {
+  extern __shared__ __align__(128) unsigned char dynamic[];
+  RingShared& s = *reinterpret_cast<RingShared*>(dynamic);
+  unsigned char* ring = dynamic + kSharedBytes;
+  const VocabArgs& v = a.v;
+  const uint32_t ctas = cluster_size(), cta = cluster_rank();
+  const uint32_t per = (v.cut.chunks + ctas - 1) / ctas;
+  const uint32_t lo = min(v.cut.chunks, cta * per), hi = min(v.cut.chunks, lo + per);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kMaxSlots; ++i) {
+      dev::mbar_init(&s.full[i], 1);
+      dev::mbar_init(&s.empty[i], kGradWarps);
+    }
+    for (uint32_t i = 0; i < kSets; ++i) dev::mbar_init(&s.done[i], kGradWarps);
+    for (uint32_t i = 0; i < kJoins; ++i) dev::mbar_init(&s.joined[i], kSumWarps + ctas);
+    dev::mbar_init(&s.never, 1);
+    s.abort = 0;
+    dev::fence_mbar_init();
+  }
+  __syncthreads();
+  start(ctas);
+  if (threadIdx.x == 0) dev::record_sm(v.sm_mask);
+  Rows rows;
+  rows.first = blockIdx.x / ctas;
+  rows.step = gridDim.x / ctas;
+  rows.count = static_cast<uint32_t>((v.rows - rows.first + rows.step - 1) / rows.step);
+  const Wait wait{&s.abort, a.status, a.timeout_ns};
+  const uint32_t warp = threadIdx.x >> 5;
+  if (warp < kSumWarps) sum_warp<DT>(a, s, ring, rows, cta, ctas, lo, hi, wait);
+  else if (warp < kLoaderWarp) grad_warp<DT>(a, s, ring, rows, cta, ctas, lo, hi, wait);
+  else if (warp == kLoaderWarp) loader_warp<DT>(a, s, ring, rows, lo, hi, wait);
+  else teacher_warp<DT>(a, s, rows, cta, ctas, lo, hi, wait);
+  __syncwarp();
+  if (ctas > 1) cluster_barrier();
+}
+
+template <int DT>
+cudaError_t ask_clusters(int cluster, size_t smem, int* n) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(cluster) * 64);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaOccupancyMaxActiveClusters(n, distill_ring_kernel<DT>, &cfg);
+}
+
+template <int DT>
+bool plan_t(DistillArgs& a, VocabLaunch& l) {
+  VocabArgs& v = a.v;
+  set_cut<DT>(v, 2);
+  const uint32_t n = v.cut.chunks;
+  // short rows: a row's latency (about 3 us of joins and barriers) is not
+  // covered by its bytes, and the kernel that reads twice has more rows in flight
+  if (n < kMinChunks) return false;
+  if (l.smem_optin < kSharedBytes) return false;
+  const size_t room = l.smem_optin - kSharedBytes;
+  const auto slot_bytes = [&](int c) { return static_cast<size_t>((n + c - 1) / c) * (kChunkVectors * 16) + v.used * 16; };
+  const auto slots = [&](int c) {
+    return static_cast<int>(room / slot_bytes(c) < kMaxSlots ? room / slot_bytes(c) : kMaxSlots);
+  };
+  // the smallest cluster whose slots hold three slices: small clusters leave
+  // the fewest SMs without one. With fewer rows than clusters, larger ones.
+  int c = 1;
+  while (c < kRingMaxCluster && slots(c) < kMinSlots) ++c;
+  if (slots(c) < kMinSlots || (l.cap > 0 && l.cap < c)) return false;
+  while (2 * c <= kRingMaxCluster && v.rows * 2 * c <= static_cast<uint64_t>(l.sm_count) && n >= 2 * c * kMinChunks &&
+         (l.cap <= 0 || 2 * c <= l.cap))
+    c *= 2;
+  a.slots = slots(c);
+  a.slot_bytes = static_cast<uint32_t>(slot_bytes(c));
+  int& fit = l.ring_clusters[(DT == kBF16 ? 1 : 0) * (kRingMaxCluster + 1) + c];
+  if (fit == 0) {
+    // asked once a group, with the most shared memory: one CTA to an SM
+    if (cudaFuncSetAttribute(distill_ring_kernel<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(l.smem_optin)) != cudaSuccess ||
+        ask_clusters<DT>(c, l.smem_optin, &fit) != cudaSuccess || fit <= 0) {
+      fit = 0;
+      cudaGetLastError();
+      return false;
+    }
+  }
+  l.cluster = c;
+  l.clusters = fit;
+  if (l.cap > 0 && l.clusters * c > l.cap) l.clusters = l.cap / c;
+  if (v.rows < static_cast<uint64_t>(l.clusters)) l.clusters = static_cast<int>(v.rows);
+  return true;
+}
+
+template <int DT>
+int launch_t(DistillArgs& a, VocabLaunch& l) {
+  a.sum_step = step_of(a.v.cut, kSumWarps);
+  a.grad_step = step_of(a.v.cut, kGradWarps);
+  // all the shared memory, so that one CTA has an SM to itself
+  return launch_rows(distill_ring_kernel<DT>, a, l, static_cast<uint64_t>(l.clusters) * l.cluster, kThreads, l.cluster,
+                     l.smem_optin);
+}
+
+}  // namespace
+
+namespace vocab {
+bool plan_distill_ring(int dtype, DistillArgs& a, VocabLaunch& l) {
+  return dtype == kBF16 ? plan_t<kBF16>(a, l) : plan_t<kF32>(a, l);
+}
+int launch_distill_ring(int dtype, DistillArgs& a, VocabLaunch& l) {
+  return dtype == kBF16 ? launch_t<kBF16>(a, l) : launch_t<kF32>(a, l);
+}
+}  // namespace vocab
+
+}  // namespace tccl

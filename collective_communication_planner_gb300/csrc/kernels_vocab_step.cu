@@ -1,0 +1,91 @@
+// Distillation with its gradient in one call.
+#include "vocab_grad.cuh"
+
+namespace tccl {
+namespace {
+
+using namespace vocab;
+
+constexpr int kThreads = 256;
+constexpr uint64_t kKeepBytes = 52ull << 20;  // rows that L2 keeps between two reads
+constexpr int kStepCluster = 8;
+constexpr int kStepCtasPerSm = 5;
+
+// Loss and gradient in one call: a cluster of CTAs sums up a row, joins its
+// statistics through distributed shared memory and reads it again, from L2,
+// for the gradient.
+template <int DT>
+__global__ void __launch_bounds__(kThreads, kStepCtasPerSm) distill_step_kernel(const __grid_constant__ DistillArgs a) {
+  __shared__ GradSegments seg;
+  __shared__ Named named;
+  __shared__ LossSlots loss;
+  __shared__ JoinSlots slots;
+  const VocabArgs& v = a.v;
+  const uint32_t ctas = cluster_size(), cta = cluster_rank();
+  const uint32_t per = (v.cut.chunks + ctas - 1) / ctas;
+  const uint32_t lo = min(v.cut.chunks, cta * per), hi = min(v.cut.chunks, lo + per);
+  start(ctas);
+  if (threadIdx.x == 0) dev::record_sm(v.sm_mask);
+  int phase = 0;
+  const float c = v.exp2_scale;
+  for (uint64_t t = blockIdx.x / ctas; t < v.rows; t += gridDim.x / ctas) {
+    __syncthreads();  // the last row's segments and columns are done with
+    set_segments<DT>(v, t, seg);
+    __syncthreads();
+    if (threadIdx.x < 32) {
+      const TeacherRow q = read_teacher(a, t);
+      uint32_t x[kMaxTop / 32];
+      load_named<DT>(v, t, q, x);
+      keep_named<DT>(v, t, q, x, a.top_k, named, lo, hi, cta == 0);
+      if (cta == 0) set_loss<DT>(q, x, loss);
+    }
+    Part p = scan_row<DT, false, true>(v, seg, lo, hi, cta == 0, KeepLoad(), [](float) {});
+    p = row_join(p, c, slots, phase, ctas);
+    const bool fast = fabsf(p.m) < -kClamp;
+    const Stats st = fast ? stats_of(p, c) : slow_stats<DT>(v, seg, lo, hi, slots, phase, cta, ctas);
+    if (cta == 0 && threadIdx.x < 32) store_loss(a, t, loss, st);
+    const float w = a.weights[t] * v.inv_temp;
+    RowGrad g;
+    g.set(v, st.max, st.log2_s, w * named.total, 0.f);
+    g.zero = w == 0.f || named.total == 0.f || st.empty();
+    // An in-place gradient may be written from here on: past the join's
+    // barrier a CTA reads its own columns only, each before it replaces it.
+    if (g.zero) zero_chunks<DT>(v, seg, lo, hi, threadIdx.x >> 5, v.step);
+    else store_chunks<DT, false>(v, seg, g, lo, hi);
+    store_edges<DT>(v, seg, g, t, cta, ctas);
+    if (!g.zero) {
+      __syncthreads();
+      store_named<DT>(v, t, named, g, w, threadIdx.x);
+    }
+  }
+}
+
+template <int DT>
+int launch_step_t(DistillArgs& a, VocabLaunch& l) {
+  VocabArgs& v = a.v;
+  set_cut<DT>(v, 2);
+  // CTAs of a row: few enough rows at once for L2 to keep them between the two
+  // reads, or as many as the SMs take of few rows; every warp gets a chunk
+  const uint64_t row_bytes = static_cast<uint64_t>(v.vocab) * Elem<DT>::kBytes;
+  const uint64_t resident = static_cast<uint64_t>(l.sm_count) * kStepCtasPerSm;
+  const auto kept = [&](int c) { return (v.rows < resident / c ? v.rows : resident / c) * row_bytes; };
+  int c = 1;
+  while (c < kStepCluster && v.cut.chunks >= static_cast<uint32_t>(2 * c * kThreads / 32) &&
+         (l.cap <= 0 || 2 * c <= l.cap) && (v.rows * 2 * c <= resident || kept(c) > kKeepBytes))
+    c *= 2;
+  uint64_t rows = v.rows;
+  if (l.cap > 0 && rows * c > static_cast<uint64_t>(l.cap)) rows = l.cap / c;
+  const uint64_t most = static_cast<uint64_t>(1) << 27;
+  return launch_rows(distill_step_kernel<DT>, a, l, (rows < most ? rows : most) * c, kThreads, c, 0);
+}
+
+}  // namespace
+
+namespace vocab {
+int launch_distill_step(int dtype, DistillArgs& a, VocabLaunch& l) {
+  if (plan_distill_ring(dtype, a, l)) return launch_distill_ring(dtype, a, l);
+  return dtype == kBF16 ? launch_step_t<kBF16>(a, l) : launch_step_t<kF32>(a, l);
+}
+}  // namespace vocab
+
+}  // namespace tccl

@@ -19,7 +19,11 @@ struct VocabCut {
   uint32_t per_segment;  // chunks of a full segment, at least 1
   uint32_t chunks;       // chunks of a row
   uint32_t edge, edges;  // edge elements of a full segment, of a row
-  uint32_t step_seg, step_part;  // a step of one chunk per warp of a CTA, in (segment, chunk) form
+};
+// a step of `warps` chunks, the warps that share a row or slice, in (segment,
+// chunk) form
+struct ChunkStep {
+  uint32_t warps, seg, part;
 };
 
 // A [rows, vocab] matrix of logits cut by columns over `used` rank buffers.
@@ -36,6 +40,7 @@ struct VocabArgs {
   float inv_temp;   // 1 / temperature
   float exp2_scale; // log2(e) / temperature
   VocabCut cut;
+  ChunkStep step;   // of all warps of a CTA
 };
 
 struct LogProbsArgs {
@@ -64,12 +69,24 @@ struct DistillArgs {
   const float* saved;         // gradient alone: the forward's stats
   int top_k;
   int teacher_bf16;
+  // ring kernel: shared-memory slots for a CTA's slices of rows, bounded waits
+  int slots;
+  uint32_t slot_bytes;
+  ChunkStep sum_step, grad_step;  // of its two kinds of warps
+  int* status;
+  uint64_t timeout_ns;
+  uint64_t inject_timeout_ns;  // test hook: > 0 makes CTA 0 wait on a barrier nothing signals
 };
+
+constexpr int kRingMaxCluster = 8;
 
 struct VocabLaunch {
   int sm_count, cap;
+  size_t smem_optin;
   void* stream;
-  int ctas, threads;  // out
+  int* ring_clusters;  // the group's cache: [dtype][cluster size], clusters that fit at once (0: not asked yet)
+  int cluster, clusters;  // plan_distill_ring's
+  int ctas, threads;      // out
 };
 
 // Each returns a cudaError_t as int.

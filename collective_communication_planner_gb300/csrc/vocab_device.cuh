@@ -80,6 +80,12 @@ __device__ __forceinline__ float max_f32(float a, float b) {
   return r;
 }
 
+// a number of the datatype from its bits
+template <int DT>
+__device__ __forceinline__ float of_bits(uint32_t x) {
+  return __uint_as_float(DT == kBF16 ? x << 16 : x);
+}
+
 template <int DT>
 __device__ __forceinline__ float load_one(const char* p) {
   if (DT == kBF16) return __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(p));
@@ -104,10 +110,10 @@ struct Vec {
     w[2] = x.z;
     w[3] = x.w;
   }
-  // a vector of clamped places: adds nothing to a row's sums
+  // -inf everywhere: adds nothing to a row's maximum and sums
   __device__ __forceinline__ void set_empty() {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = DT == kBF16 ? 0xF180F180u : 0xF1800000u;
+    for (int i = 0; i < 4; ++i) w[i] = DT == kBF16 ? 0xFF80FF80u : 0xFF800000u;
   }
   __device__ __forceinline__ void clamp() {
 #pragma unroll
@@ -297,15 +303,15 @@ __device__ __forceinline__ void set_segments(const VocabArgs& v, uint64_t t, Seg
   }
 }
 
-// The chunks `first`, `first` + warps of the CTA, ... of a row.
+// The chunks `first`, `first` + step.warps, ... of a row.
 struct ChunkWalk {
   uint32_t index, seg, part;
   __device__ __forceinline__ ChunkWalk(const VocabCut& c, uint32_t first)
       : index(first), seg(first / c.per_segment), part(first - seg * c.per_segment) {}
-  __device__ __forceinline__ void next(const VocabCut& c) {
-    index += blockDim.x >> 5;
-    seg += c.step_seg;
-    part += c.step_part;
+  __device__ __forceinline__ void next(const VocabCut& c, const ChunkStep& by) {
+    index += by.warps;
+    seg += by.seg;
+    part += by.part;
     if (part >= c.per_segment) {
       part -= c.per_segment;
       ++seg;
@@ -394,7 +400,7 @@ __device__ __forceinline__ void edge_at(const VocabArgs& v, const Segments& s, u
 template <int DT, typename F>
 __device__ __forceinline__ void each_element(const VocabArgs& v, const Segments& s, uint32_t lo, uint32_t hi,
                                              bool edges, F f) {
-  for (ChunkWalk w(v.cut, lo + (threadIdx.x >> 5)); w.index < hi; w.next(v.cut)) {
+  for (ChunkWalk w(v.cut, lo + (threadIdx.x >> 5)); w.index < hi; w.next(v.cut, v.step)) {
     Vec<DT> x[kBatch];
     load_chunk<DT, true>(v, s.at<DT>(w.seg, s.head[w.seg]), w, x, StreamLoad());
 #pragma unroll
@@ -514,7 +520,7 @@ __device__ __forceinline__ Part scan_row(const VocabArgs& v, const Segments& seg
   Part a{kClamp, 0.f, 0.f};
   float r = __fmul_rn(kClamp, c);
   f32x2 s[2] = {0, 0}, u[2] = {0, 0};
-  for (ChunkWalk w(v.cut, lo + (threadIdx.x >> 5)); w.index < hi; w.next(v.cut)) {
+  for (ChunkWalk w(v.cut, lo + (threadIdx.x >> 5)); w.index < hi; w.next(v.cut, v.step)) {
     Vec<DT> x[kBatch];
     load_chunk<DT, ANY>(v, seg.at<DT>(w.seg, seg.head[w.seg]), w, x, load_vector);
     top_of(add_chunk<DT, ENTROPY>(a, r, s, u, x, c));
@@ -547,49 +553,76 @@ struct TeacherRow {
   float total;
 };
 
-__device__ __forceinline__ TeacherRow read_teacher(const DistillArgs& a, uint64_t t) {
-  constexpr int N = kMaxTop / 32;
-  const int lane = threadIdx.x & 31;
-  TeacherRow r;
-  float top = -INFINITY;
+// one logit of row t
+template <int DT>
+__device__ __forceinline__ float read_column(const VocabArgs& v, uint64_t t, uint32_t column) {
+  const uint32_t seg = column / v.shard;
+  return load_one<DT>(static_cast<const char*>(v.p.src[seg]) +
+                      (t * v.src_stride + column - seg * v.shard) * Elem<DT>::kBytes);
+}
+
+// A row's entries as they are in memory, so that what loads them can do other
+// work before the first use.
+struct TeacherEntries {
+  int64_t id[kMaxTop / 32];
+  uint32_t logit[kMaxTop / 32];  // bits of the datatype
+  float lse;
+};
+
+__device__ __forceinline__ TeacherEntries load_teacher(const DistillArgs& a, uint64_t t) {
+  TeacherEntries r;
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int k = 32 * i + lane;
-    r.column[i] = -1;
-    r.log_q[i] = -INFINITY;
+  for (int i = 0; i < kMaxTop / 32; ++i) {
+    const int k = 32 * i + (threadIdx.x & 31);
+    r.id[i] = -1;
+    r.logit[i] = 0;
     if (k < a.top_k) {
       const uint64_t o = t * a.top_k + k;
-      const int64_t id = a.ids[o];
-      if (id >= 0 && id < a.v.vocab) {
-        r.column[i] = static_cast<int32_t>(id);
-        const float x = a.teacher_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.teacher)[o])
-                                       : static_cast<const float*>(a.teacher)[o];
-        r.log_q[i] = x * a.v.inv_temp;
-      }
+      r.id[i] = a.ids[o];
+      if (a.teacher_bf16) r.logit[i] = static_cast<const uint16_t*>(a.teacher)[o];
+      else r.logit[i] = static_cast<const uint32_t*>(a.teacher)[o];
     }
-    top = fmaxf(top, r.log_q[i]);
   }
-  float lse;
-  if (a.teacher_lse) {
-    lse = a.teacher_lse[t];
-  } else {
+  r.lse = a.teacher_lse ? a.teacher_lse[t] : 0.f;
+  return r;
+}
+
+__device__ __forceinline__ TeacherRow teacher_row(const DistillArgs& a, const TeacherEntries& e) {
+  constexpr int N = kMaxTop / 32;
+  TeacherRow r;
+  float lse = e.lse, z[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const bool has = e.id[i] >= 0 && e.id[i] < a.v.vocab;
+    const float x = __uint_as_float(a.teacher_bf16 ? e.logit[i] << 16 : e.logit[i]);
+    r.column[i] = has ? static_cast<int32_t>(e.id[i]) : -1;
+    z[i] = has ? x * a.v.inv_temp : -INFINITY;
+  }
+  if (!a.teacher_lse) {
+    float top = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) top = fmaxf(top, z[i]);
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
     if (top == -INFINITY) top = 0.f;
-    float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) sum += expf(r.log_q[i] - top);
+    for (int i = 0; i < N; ++i)
+      if (32 * i < a.top_k) sum += expf(z[i] - top);
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
     lse = sum == 0.f ? 0.f : top + logf(sum);
   }
   r.total = 0.f;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    r.log_q[i] -= lse;
-    r.q[i] = expf(r.log_q[i]);
+    r.log_q[i] = z[i] - lse;
+    r.q[i] = 32 * i < a.top_k ? expf(r.log_q[i]) : 0.f;
     r.total += r.q[i];
   }
   for (int o = 16; o > 0; o >>= 1) r.total += __shfl_xor_sync(0xFFFFFFFFu, r.total, o);
   return r;
+}
+
+__device__ __forceinline__ TeacherRow read_teacher(const DistillArgs& a, uint64_t t) {
+  return teacher_row(a, load_teacher(a, t));
 }
 
 // What the loss needs of the entries, in shared memory: warp 0 writes it, with
@@ -599,13 +632,29 @@ struct LossSlots {
 };
 
 template <int DT>
-__device__ __forceinline__ void set_loss(const VocabArgs& v, const Segments& s, const TeacherRow& r, LossSlots& l) {
+__device__ __forceinline__ void set_loss(const TeacherRow& r, const uint32_t (&x)[kMaxTop / 32], LossSlots& l) {
 #pragma unroll
   for (int i = 0; i < kMaxTop / 32; ++i) {
     const int k = 32 * i + (threadIdx.x & 31);
     l.q[k] = r.q[i];
     l.log_q[k] = r.log_q[i];
-    l.x[k] = r.column[i] >= 0 ? load_one<DT>(s.at_column<DT>(v, r.column[i])) : 0.f;
+    l.x[k] = of_bits<DT>(x[i]);
+  }
+}
+
+// The bits of the student's logits at the entries' columns, all loads issued
+// together; of_bits when they are used.
+template <int DT>
+__device__ __forceinline__ void load_named(const VocabArgs& v, uint64_t t, const TeacherRow& r,
+                                           uint32_t (&x)[kMaxTop / 32]) {
+#pragma unroll
+  for (int i = 0; i < kMaxTop / 32; ++i) {
+    x[i] = 0;
+    if (r.column[i] < 0) continue;
+    const uint32_t seg = r.column[i] / v.shard;
+    const uint64_t o = t * v.src_stride + r.column[i] - seg * v.shard;
+    if (DT == kBF16) x[i] = static_cast<const uint16_t*>(v.p.src[seg])[o];
+    else x[i] = static_cast<const uint32_t*>(v.p.src[seg])[o];
   }
 }
 
@@ -649,19 +698,21 @@ inline void set_cut(VocabArgs& v, int spare) {
   if (v.used == 1) c.per_segment = c.chunks > 0 ? c.chunks : 1;
 }
 
-inline void set_step(VocabCut& c, int threads) {
-  c.step_seg = threads / 32 / c.per_segment;
-  c.step_part = threads / 32 % c.per_segment;
+inline ChunkStep step_of(const VocabCut& c, uint32_t warps) {
+  return ChunkStep{warps, warps / c.per_segment, warps % c.per_segment};
 }
 
-int launch_distill_forward(int dtype, DistillArgs& a, VocabLaunch& l);
+int launch_distill_step(int dtype, DistillArgs& a, VocabLaunch& l);
+// whether the ring kernel takes the call; sets its plan in a and l
+bool plan_distill_ring(int dtype, DistillArgs& a, VocabLaunch& l);
+int launch_distill_ring(int dtype, DistillArgs& a, VocabLaunch& l);
 
 // Launches `kernel` on clusters of `cluster` CTAs; uncapped calls start early
 // (the kernel waits before it touches memory).
 template <typename Kernel, typename Args>
 inline int launch_rows(Kernel kernel, Args& a, VocabLaunch& l, uint64_t grid, int threads, int cluster,
                        size_t smem) {
-  set_step(a.v.cut, threads);
+  a.v.step = step_of(a.v.cut, threads / 32);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(static_cast<unsigned>(threads));

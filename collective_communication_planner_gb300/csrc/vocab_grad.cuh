@@ -1,0 +1,258 @@
+// Device code shared by the kernels that write gradients of
+// vocabulary-parallel logits.
+#pragma once
+
+#include "vocab_device.cuh"
+
+namespace tccl {
+namespace vocab {
+
+// The segments of the current row for a gradient: where the logits and the
+// gradient start, and the first element of the body, which starts on a 16-byte
+// boundary of the gradient. Where the logits do not, a vector is put together
+// from two aligned ones, and the body leaves both ends of the segment enough
+// elements that those lie within it.
+struct GradSegments : Segments {
+  char* dst[kMaxRanks];
+  template <int DT>
+  __device__ __forceinline__ char* to(uint32_t seg, uint32_t col) const {
+    return dst[seg] + static_cast<uint64_t>(col) * Elem<DT>::kBytes;
+  }
+};
+
+template <int DT>
+__device__ __forceinline__ uint32_t head_of(const char* dst) {
+  return static_cast<uint32_t>(-reinterpret_cast<uintptr_t>(dst) & 15) / Elem<DT>::kBytes + Elem<DT>::kVec;
+}
+
+template <int DT>
+__device__ __forceinline__ void set_segment(const VocabArgs& v, uint64_t t, uint32_t r, GradSegments& s) {
+  s.src[r] = static_cast<const char*>(v.p.src[r]) + t * v.src_stride * Elem<DT>::kBytes;
+  char* dst = static_cast<char*>(v.p.dst[r]) + t * v.dst_stride * Elem<DT>::kBytes;
+  s.dst[r] = dst;
+  s.head[r] = v.aligned ? 0 : head_of<DT>(dst);
+}
+
+// thread r < used sets rank r's segment of row t; the caller synchronises
+template <int DT>
+__device__ __forceinline__ void set_segments(const VocabArgs& v, uint64_t t, GradSegments& s) {
+  if (threadIdx.x < v.used) set_segment<DT>(v, t, threadIdx.x, s);
+}
+
+// One row's gradient y = p (scale + slope log2 p); columns that a token or a
+// teacher's entry names get their own term afterwards.
+// log2 p = x c - (max c + log2_s): the subtrahend is rounded once (hi), so
+// that it takes one fused operation an element, and what the rounding lost is
+// made up for in scale and slope. A row whose maximum is not within
+// (-2^100, 2^100) is not `fast`: (x - max) c - log2_s then.
+struct RowGrad {
+  float max, c, log2_s, hi, scale, slope, fast_scale, fast_slope;
+  bool zero, fast;
+
+  __device__ __forceinline__ void set(const VocabArgs& v, float m, float log2_sum, float to_scale, float to_slope) {
+    max = m;
+    c = v.exp2_scale;
+    log2_s = log2_sum;
+    fast = fabsf(m) < -kClamp;
+    scale = to_scale;
+    slope = to_slope;
+    const float mc = __fmul_rn(m, c);
+    hi = __fadd_rn(mc, log2_s);
+    // max c + log2_s - hi: the product's rounding, and the sum's (two-sum)
+    const float back = __fsub_rn(hi, mc);
+    const float lost = __fadd_rn(__fadd_rn(__fsub_rn(mc, __fsub_rn(hi, back)), __fsub_rn(log2_s, back)),
+                                 __fmaf_rn(m, c, -mc));
+    const float f = exp2_ftz(-lost);
+    fast_scale = f * __fmaf_rn(-slope, lost, scale);
+    fast_slope = f * slope;
+  }
+  __device__ __forceinline__ float one(float x) const {
+    const float l = fast ? __fmaf_rn(x, c, -hi) : (x - max) * c - log2_s, p = exp2_ftz(l);
+    const float s = fast ? fast_slope : slope, o = fast ? fast_scale : scale;
+    // a masked place: 0 whatever its distance
+    return p == 0.f ? 0.f : p * (s == 0.f ? o : __fmaf_rn(s, l, o));
+  }
+  template <bool SLOPE>
+  __device__ __forceinline__ f32x2 two(f32x2 x) const {
+    const f32x2 l = fma2(x, pack(c, c), pack(-hi, -hi));
+    const f32x2 p = exp2x2(l);
+    if (!SLOPE) return mul2(p, pack(fast_scale, fast_scale));
+    return mul2(p, fma2(pack(fast_slope, fast_slope), l, pack(fast_scale, fast_scale)));
+  }
+};
+
+// The gradient of a vector of the row. A named column's own term is not in it:
+// a branch for it here would keep the vectors of a chunk from overlapping
+// (GB300, 4096 x 131072 bf16: 452 us with it, 314 without).
+template <int DT, bool SLOPE, bool FAST>
+__device__ __forceinline__ uint4 grad_of(const RowGrad& g, Vec<DT>& x) {
+  Vec<DT> y;
+  if (FAST) {
+    if (SLOPE) x.clamp();  // a masked place: 0 times a finite distance
+#pragma unroll
+    for (int i = 0; i < Vec<DT>::kPairs; ++i) y.put_pair(i, g.two<SLOPE>(x.pair(i)));
+  } else {
+#pragma unroll
+    for (int i = 0; i < Vec<DT>::kPairs; ++i) y.put_pair(i, pack(g.one(x.get(2 * i)), g.one(x.get(2 * i + 1))));
+  }
+  return y.out();
+}
+
+// Stores the gradient of a lane's vectors of a chunk; `first` is the lane's
+// first vector of the segment's `end`, and goes to `to`.
+template <int DT, bool SLOPE, bool FAST>
+__device__ __forceinline__ void store_chunk(const RowGrad& g, Vec<DT> (&x)[kBatch], char* to, uint32_t first,
+                                            uint32_t end) {
+  if (first - (threadIdx.x & 31) + kChunkVectors <= end) {
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) dev::st_global_v4(to + k * 512, grad_of<DT, SLOPE, FAST>(g, x[k]));
+  } else {
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      if (first + k * 32 < end) dev::st_global_v4(to + k * 512, grad_of<DT, SLOPE, FAST>(g, x[k]));
+  }
+}
+
+// The gradient of this warp's chunks of [lo, hi) of the row. In place a lane
+// reads a vector before it replaces it, and no other lane reads it: the
+// buffers are equally aligned then.
+template <int DT, bool SLOPE, bool FAST>
+__device__ __forceinline__ void store_chunks(const VocabArgs& v, const GradSegments& s, const RowGrad& g, uint32_t lo,
+                                             uint32_t hi) {
+  for (ChunkWalk w(v.cut, lo + (threadIdx.x >> 5)); w.index < hi; w.next(v.cut, v.step)) {
+    Vec<DT> x[kBatch];
+    const uint32_t first = w.vector(), head = s.head[w.seg];
+    load_chunk<DT, true>(v, s.at<DT>(w.seg, head), w, x, StreamLoad());
+    store_chunk<DT, SLOPE, FAST>(g, x, s.to<DT>(w.seg, head) + static_cast<uint64_t>(first) * 16, first, w.vectors(v));
+  }
+}
+template <int DT, bool SLOPE>
+__device__ __forceinline__ void store_chunks(const VocabArgs& v, const GradSegments& s, const RowGrad& g, uint32_t lo,
+                                             uint32_t hi) {
+  if (g.fast) store_chunks<DT, SLOPE, true>(v, s, g, lo, hi);
+  else store_chunks<DT, SLOPE, false>(v, s, g, lo, hi);
+}
+
+template <int DT>
+__device__ __forceinline__ void zero_chunks(const VocabArgs& v, const GradSegments& s, uint32_t lo, uint32_t hi,
+                                            uint32_t warp, const ChunkStep& step) {
+  for (ChunkWalk w(v.cut, lo + warp); w.index < hi; w.next(v.cut, step)) {
+    const uint32_t first = w.vector(), end = w.vectors(v);
+    char* to = s.to<DT>(w.seg, s.head[w.seg]) + static_cast<uint64_t>(first) * 16;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      if (first + k * 32 < end) dev::st_global_v4(to + k * 512, make_uint4(0, 0, 0, 0));
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ void zero_padding(const VocabArgs& v, uint64_t t, uint32_t first, uint32_t step) {
+  const uint32_t all = v.nranks * v.shard;
+  for (uint32_t j = v.vocab + first; j < all; j += step) {
+    const uint32_t r = j / v.shard;
+    store_one<DT>(static_cast<char*>(v.p.dst[r]) + (t * v.dst_stride + (j - r * v.shard)) * Elem<DT>::kBytes, 0.f);
+  }
+}
+
+// The edge elements of the row, by CTA 0 of the row's, and the zeros of its
+// padding columns, shared by all of them.
+template <int DT>
+__device__ __forceinline__ void store_edges(const VocabArgs& v, const GradSegments& s, const RowGrad& g, uint64_t t,
+                                            uint32_t cta, uint32_t ctas) {
+  for (uint32_t e = threadIdx.x; cta == 0 && e < v.cut.edges; e += blockDim.x) {
+    uint32_t seg, col;
+    edge_at<DT>(v, s, e, seg, col);
+    store_one<DT>(s.to<DT>(seg, col), g.zero ? 0.f : g.one(load_one<DT>(s.at<DT>(seg, col))));
+  }
+  zero_padding<DT>(v, t, cta * blockDim.x + threadIdx.x, ctas * blockDim.x);
+}
+
+// the chunk that a column of row t is in, or kEdge
+constexpr uint32_t kEdge = 0xFFFFFFFFu;
+template <int DT>
+__device__ __forceinline__ uint32_t chunk_of(const VocabArgs& v, uint64_t t, uint32_t column) {
+  const uint32_t seg = column / v.shard, col = column - seg * v.shard;
+  const char* dst = static_cast<const char*>(v.p.dst[seg]) + t * v.dst_stride * Elem<DT>::kBytes;
+  const uint32_t head = v.aligned ? 0 : head_of<DT>(dst);
+  const uint32_t vectors = seg + 1 == v.used ? v.cut.last : v.cut.full, vec = (col - head) / Elem<DT>::kVec;
+  if (col < head || vec >= vectors) return kEdge;
+  return seg * v.cut.per_segment + vec / kChunkVectors;
+}
+
+// whether a CTA that has chunks [lo, hi) of row t, and with `edges` the edge
+// elements, has a column
+template <int DT>
+__device__ __forceinline__ bool has_column(const VocabArgs& v, uint64_t t, uint32_t column, uint32_t lo, uint32_t hi,
+                                           bool edges) {
+  const uint32_t chunk = chunk_of<DT>(v, t, column);
+  return chunk == kEdge ? edges : chunk >= lo && chunk < hi;
+}
+
+template <int DT>
+__device__ __forceinline__ void write_column(const VocabArgs& v, uint64_t t, uint32_t column, float y) {
+  const uint32_t seg = column / v.shard;
+  store_one<DT>(static_cast<char*>(v.p.dst[seg]) + (t * v.dst_stride + column - seg * v.shard) * Elem<DT>::kBytes, y);
+}
+
+// The teacher's columns that fall to this CTA, in entry order: after the
+// body's stores those columns get their own value.
+struct Named {
+  alignas(16) int32_t column[kMaxTop];
+  float q[kMaxTop], x[kMaxTop];
+  float total;
+  int count;
+};
+
+// Warp 0 keeps the entries of the row whose column is in chunks [lo, hi), or,
+// with `edges`, an edge element, in entry order, with the logits there, since an
+// in-place gradient replaces them.
+template <int DT>
+__device__ __forceinline__ void keep_named(const VocabArgs& v, uint64_t t, const TeacherRow& r,
+                                           const uint32_t (&x)[kMaxTop / 32], int top_k, Named& n, uint32_t lo,
+                                           uint32_t hi, bool edges) {
+  int count = 0;
+#pragma unroll
+  for (int i = 0; i < kMaxTop / 32; ++i) {
+    if (32 * i >= top_k) break;
+    const bool here = r.column[i] >= 0 && has_column<DT>(v, t, r.column[i], lo, hi, edges);
+    const uint32_t mask = __ballot_sync(0xFFFFFFFFu, here);
+    if (here) {
+      const int at = count + __popc(mask & ((1u << (threadIdx.x & 31)) - 1));
+      n.column[at] = r.column[i];
+      n.q[at] = r.q[i];
+      n.x[at] = of_bits<DT>(x[i]);
+    }
+    count += __popc(mask);
+  }
+  // columns are looked through four at a time
+  if ((threadIdx.x & 31) < 3 && count + (threadIdx.x & 31) < kMaxTop) n.column[count + (threadIdx.x & 31)] = -1;
+  if ((threadIdx.x & 31) == 0) {
+    n.count = count;
+    n.total = r.total;
+  }
+}
+
+// after a barrier behind the body's stores
+template <int DT>
+__device__ __forceinline__ void store_named(const VocabArgs& v, uint64_t t, const Named& n, const RowGrad& g, float weight,
+                                            int i) {
+  if (i >= n.count) return;
+  const int32_t column = n.column[i];
+  float q = 0.f;
+  bool first = true;  // or an earlier entry names it too and does this
+  for (int j = 0; j < n.count; j += 4) {
+    const int4 c = *reinterpret_cast<const int4*>(&n.column[j]);
+    const int32_t four[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (four[k] == column) {
+        first = first && j + k >= i;
+        q += n.q[j + k];
+      }
+  }
+  if (!first) return;
+  write_column<DT>(v, t, column, g.one(n.x[i]) - q * weight);
+}
+
+}  // namespace vocab
+}  // namespace tccl

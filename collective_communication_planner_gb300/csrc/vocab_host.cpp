@@ -1,7 +1,6 @@
 // C entry points of the operators over vocabulary-parallel logits
 // (include/tccl.h): argument validation and launches. Host code only; the
-// kernels are in kernels_vocab_forward.cu and
-// kernels_vocab_grad.cu.
+// kernels are in kernels_vocab_*.cu.
 #include "vocab.h"
 
 #include <cuda_runtime.h>
@@ -127,7 +126,7 @@ tcclResult_t run(tcclGroup* g, int (*launch)(int, Args&, VocabLaunch&), Args& a,
   if (cur != g->device && cudaSetDevice(g->device) != cudaSuccess) return tcclCudaError;
   a.v.sm_mask = sm_record_slot(g);
   std::memset(&g->last, 0, sizeof(g->last));
-  VocabLaunch l{g->dev.sm_count, cap, stream, 0, 0};
+  VocabLaunch l{g->dev.sm_count, cap, (size_t)g->dev.smem_optin, stream, g->ring_clusters, 0, 0, 0, 0};
   const int err = launch(dtype, a, l);
   g->last.ctas = l.ctas;
   g->last.threads = l.threads;
@@ -237,6 +236,9 @@ tcclResult_t tcclDistill(tcclGroup_t g, const void* const logits[], const tcclVo
   a.loss = loss;
   a.stats = stats;
   a.weights = weights;
+  a.status = g->d_status;
+  a.timeout_ns = (uint64_t)(g->cfg.wait_timeout_ms * 1e6);
+  a.inject_timeout_ns = g->inject_ns;
   return run(g, launch_distill, a, shape->datatype, cta_cap, stream);
 }
 
