@@ -336,7 +336,7 @@ template <int DT>
 __global__ void __launch_bounds__(kThreads, 5) distill_kernel(const __grid_constant__ DistillArgs a) {
   __shared__ Segments seg;
   __shared__ JoinSlots slots;
-  __shared__ LossSlots loss;
+  __shared__ Entries entries;
   const VocabArgs& v = a.v;
   const uint32_t ctas = cluster_size(), cta = cluster_rank();
   const uint32_t per = (v.cut.chunks + ctas - 1) / ctas;
@@ -353,11 +353,11 @@ __global__ void __launch_bounds__(kThreads, 5) distill_kernel(const __grid_const
       const TeacherRow q = read_teacher(a, t);
       uint32_t x[kMaxTop / 32];
       load_named<DT>(v, t, q, x);
-      set_loss<DT>(q, x, loss);
+      set_entries<DT>(q, x, a.top_k, entries, [](uint32_t) { return false; });
     }
     float unused;
     const Stats st = row_stats<DT, false, false>(v, seg, lo, hi, cta, ctas, slots, phase, nullptr, 0, unused);
-    if (mine) store_loss(a, t, loss, st);
+    if (mine) store_loss(a, t, entries, st);
   }
 }
 

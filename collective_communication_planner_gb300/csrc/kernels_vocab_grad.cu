@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(kThreads, 5) log_probs_grad_kernel(const __gri
 template <int DT>
 __global__ void __launch_bounds__(kThreads, 5) distill_grad_kernel(const __grid_constant__ DistillArgs a) {
   __shared__ GradSegments seg;
-  __shared__ Named named;
+  __shared__ Entries named;
   const VocabArgs& v = a.v;
   start(1);
   if (threadIdx.x == 0) dev::record_sm(v.sm_mask);
@@ -71,7 +71,9 @@ __global__ void __launch_bounds__(kThreads, 5) distill_grad_kernel(const __grid_
       const TeacherRow q = read_teacher(a, t);
       uint32_t x[kMaxTop / 32];
       load_named<DT>(v, t, q, x);
-      keep_named<DT>(v, t, q, x, a.top_k, named, it.lo, it.hi, it.part == 0);
+      set_entries<DT>(q, x, a.top_k, named, [&](uint32_t column) {
+        return has_column<DT>(v, t, column, it.lo, it.hi, it.part == 0);
+      });
     }
     __syncthreads();
     zero = zero || named.total == 0.f;
@@ -83,7 +85,7 @@ __global__ void __launch_bounds__(kThreads, 5) distill_grad_kernel(const __grid_
     store_edges<DT>(v, seg, g, t, it.part, v.parts);
     if (!zero) {
       __syncthreads();
-      store_named<DT>(v, t, named, g, w, threadIdx.x);
+      if (threadIdx.x < named.count) store_named<DT>(v, t, named, g, w, threadIdx.x);
     }
   }
 }
@@ -91,7 +93,7 @@ __global__ void __launch_bounds__(kThreads, 5) distill_grad_kernel(const __grid_
 template <int DT, typename Args>
 int launch_parts(void (*kernel)(Args), Args& a, VocabLaunch& l) {
   VocabArgs& v = a.v;
-  set_cut<DT>(v, 2);
+  set_cut<DT>(v, v.together ? 0 : 2);
   // an item is at most eight chunks a warp; fewer where that leaves SMs
   // without four items
   constexpr uint32_t kWarps = kThreads / 32;

@@ -21,7 +21,7 @@ namespace {
 
 using namespace vocab;
 
-constexpr uint32_t kSumWarps = 12, kGradWarps = 12;
+constexpr uint32_t kSumWarps = 8, kGradWarps = 8;
 constexpr uint32_t kTeacherWarps = 3;  // they take the rows in turn
 constexpr uint32_t kLoaderWarp = kSumWarps + kGradWarps, kFirstTeacher = kLoaderWarp + 1;
 constexpr int kThreads = (kFirstTeacher + kTeacherWarps) * 32;
@@ -31,6 +31,7 @@ constexpr int kMinSlots = 3, kMaxSlots = 4;
 // warp sets row n + 3's up before it is done with row n, and row n + 6's after
 // that: every warp that reads row n's set is past it then.
 constexpr uint32_t kSets = 2 * kTeacherWarps;
+constexpr uint32_t kEdgeBatch = 4;  // edge elements whose loads a lane issues together
 // The parts of a row, row n's being set n % kJoins: from every CTA of the
 // cluster the sum warps' and, as the last, the edge elements' from the row's
 // teacher warp. A warp of another CTA sends row n only when all have sent row
@@ -49,9 +50,8 @@ struct RingShared {
                               // teacher warps' arrivals, the other sum warps' bytes
   uint64_t never;             // test hook
   float2 part[kJoins][kRingMaxCluster * kParts];  // maximum and sum
-  GradSegments seg[kMaxSlots], edge_seg[kTeacherWarps];
-  Named named[kSets];
-  LossSlots loss[kSets];
+  GradSegments seg[kMaxSlots];
+  Entries named[kSets];
   float weight[kSets];
   int abort;
 };
@@ -372,18 +372,26 @@ __device__ void loader_warp(const DistillArgs& a, RingShared& s, unsigned char* 
   for (uint32_t r = n > slots ? n - slots : 0; r < n; ++r) wait(&s.full[r % slots], r / slots, false);
 }
 
+// the column of edge element `e` of row t
+template <int DT>
+__device__ __forceinline__ uint32_t edge_column(const VocabArgs& v, uint64_t t, uint32_t e) {
+  uint32_t seg = v.used - 1, vectors = v.cut.last;
+  if (e < seg * v.cut.edge) {
+    seg = e / v.cut.edge;
+    vectors = v.cut.full;
+  }
+  const char* dst = static_cast<const char*>(v.p.dst[seg]) + t * v.dst_stride * Elem<DT>::kBytes;
+  uint32_t col = e - seg * v.cut.edge;
+  if (col >= head_of<DT>(v, dst)) col += vectors * Elem<DT>::kVec;
+  return seg * v.shard + col;
+}
+
 template <int DT>
 __device__ void teacher_warp(const DistillArgs& a, RingShared& s, const Rows& rows, uint32_t cta, uint32_t ctas,
                              uint32_t lo, uint32_t hi, const Wait& wait) {
   const VocabArgs& v = a.v;
   const float c = v.exp2_scale;
   const uint32_t lane = threadIdx.x & 31, mine = (threadIdx.x >> 5) - kFirstTeacher;
-  GradSegments& edge_seg = s.edge_seg[mine];
-  const auto set_edges = [&](uint64_t t) {
-    __syncwarp();
-    for (uint32_t r = lane; r < v.used; r += 32) set_segment<DT>(v, t, r, edge_seg);
-    __syncwarp();
-  };
   // A row's loads are issued an iteration (three rows) before they are used:
   // its entries, then the logits at their columns. `entries` and `weight` are the
   // next row's to be begun, q and x the one's begun.
@@ -408,20 +416,24 @@ __device__ void teacher_warp(const DistillArgs& a, RingShared& s, const Rows& ro
   const auto finish = [&](uint32_t n) {
     if (n >= rows.count) return;
     const uint64_t t = rows.row(n);
-    keep_named<DT>(v, t, q, x, a.top_k, s.named[n % kSets], lo, hi, cta == 0);
+    set_entries<DT>(q, x, a.top_k, s.named[n % kSets], [&](uint32_t column) {
+      return has_column<DT>(v, t, column, lo, hi, cta == 0);
+    });
     Part p{-INFINITY, 0.f, 0.f};
     if (cta == 0) {
-      set_loss<DT>(q, x, s.loss[n % kSets]);
-      if (v.cut.edges) set_edges(t);
-      for (uint32_t e = lane; e < v.cut.edges; e += 32) {
-        uint32_t seg, col;
-        edge_at<DT>(v, edge_seg, e, seg, col);
-        const float y = load_one<DT>(edge_seg.at<DT>(seg, col));
-        if (y > p.m) {
-          p.s *= exp2_ftz((p.m - y) * c);
-          p.m = y;
+      for (uint32_t e = lane; e < v.cut.edges; e += 32 * kEdgeBatch) {
+        float y[kEdgeBatch];
+#pragma unroll
+        for (uint32_t i = 0; i < kEdgeBatch; ++i)
+          y[i] = e + 32 * i < v.cut.edges ? read_column<DT>(v, t, edge_column<DT>(v, t, e + 32 * i)) : -INFINITY;
+#pragma unroll
+        for (uint32_t i = 0; i < kEdgeBatch; ++i) {
+          if (y[i] > p.m) {
+            p.s *= exp2_ftz((p.m - y[i]) * c);
+            p.m = y[i];
+          }
+          if (y[i] != -INFINITY) p.s += exp2_ftz((y[i] - (p.m == -INFINITY ? 0.f : p.m)) * c);
         }
-        if (y != -INFINITY) p.s += exp2_ftz((y - (p.m == -INFINITY ? 0.f : p.m)) * c);
       }
     }
     p = join_lanes_any(p, c);
@@ -439,18 +451,22 @@ __device__ void teacher_warp(const DistillArgs& a, RingShared& s, const Rows& ro
     load(n + 2 * kTeacherWarps);
     if (!wait(&s.joined[n % kJoins], n / kJoins)) return;
     const Stats st = row_parts(s, n, ctas, c);
-    const Named& named = s.named[n % kSets];
+    const Entries& named = s.named[n % kSets];
     const float w = s.weight[n % kSets];
     RowGrad g;
     g.set(v, st.max, st.log2_s, w * named.total, 0.f);
     g.zero = w == 0.f || named.total == 0.f || st.empty();
     if (cta == 0) {
-      store_loss(a, t, s.loss[n % kSets], st);
-      if (v.cut.edges) set_edges(t);
-      for (uint32_t e = lane; e < v.cut.edges; e += 32) {
-        uint32_t seg, col;
-        edge_at<DT>(v, edge_seg, e, seg, col);
-        store_one<DT>(edge_seg.to<DT>(seg, col), g.zero ? 0.f : g.one(load_one<DT>(edge_seg.at<DT>(seg, col))));
+      store_loss(a, t, named, st);
+      for (uint32_t e = lane; e < v.cut.edges; e += 32 * kEdgeBatch) {
+        float y[kEdgeBatch];
+#pragma unroll
+        for (uint32_t i = 0; i < kEdgeBatch; ++i)
+          if (e + 32 * i < v.cut.edges) y[i] = read_column<DT>(v, t, edge_column<DT>(v, t, e + 32 * i));
+#pragma unroll
+        for (uint32_t i = 0; i < kEdgeBatch; ++i)
+          if (e + 32 * i < v.cut.edges)
+            write_column<DT>(v, t, edge_column<DT>(v, t, e + 32 * i), g.zero ? 0.f : g.one(y[i]));
       }
     }
     finish(n + kTeacherWarps);
@@ -500,12 +516,16 @@ __global__ void __launch_bounds__(kThreads, 1) distill_ring_kernel(const __grid_
   if (ctas > 1) cluster_barrier();
 }
 
+// How many clusters of this size run at once, a CTA to an SM: asked once a
+// group, 0 if the device cannot say.
 template <int DT>
-cudaError_t ask_clusters(int cluster, size_t smem, int* n) {
+int clusters_that_fit(int cluster, VocabLaunch& l) {
+  int& fit = l.ring_clusters[(DT == kBF16 ? 1 : 0) * (kRingMaxCluster + 1) + cluster];
+  if (fit > 0) return fit;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(cluster) * 64);
+  cfg.gridDim = dim3(static_cast<unsigned>(cluster));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = l.smem_optin;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
@@ -513,13 +533,19 @@ cudaError_t ask_clusters(int cluster, size_t smem, int* n) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaOccupancyMaxActiveClusters(n, distill_ring_kernel<DT>, &cfg);
+  if (cudaFuncSetAttribute(distill_ring_kernel<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(l.smem_optin)) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&fit, distill_ring_kernel<DT>, &cfg) != cudaSuccess) {
+    fit = 0;
+    cudaGetLastError();
+  }
+  return fit;
 }
 
 template <int DT>
 bool plan_t(DistillArgs& a, VocabLaunch& l) {
   VocabArgs& v = a.v;
-  set_cut<DT>(v, 2);
+  set_cut<DT>(v, v.together ? 0 : 2);
   const uint32_t n = v.cut.chunks;
   // short rows: a row's latency (about 3 us of joins and barriers) is not
   // covered by its bytes, and the kernel that reads twice has more rows in flight
@@ -530,27 +556,27 @@ bool plan_t(DistillArgs& a, VocabLaunch& l) {
   const auto slots = [&](int c) {
     return static_cast<int>(room / slot_bytes(c) < kMaxSlots ? room / slot_bytes(c) : kMaxSlots);
   };
-  // the smallest cluster whose slots hold three slices: small clusters leave
-  // the fewest SMs without one. With fewer rows than clusters, larger ones.
-  int c = 1;
-  while (c < kRingMaxCluster && slots(c) < kMinSlots) ++c;
-  if (slots(c) < kMinSlots || (l.cap > 0 && l.cap < c)) return false;
+  // Of the clusters whose slots hold three slices, the one that leaves the
+  // fewest SMs without a CTA (GB300, one CTA to an SM: clusters of 1 to 8 fill
+  // 152, 152, 138, 144, 140, 138, 105, 120 of 152). Fewer rows than clusters:
+  // larger ones instead.
+  int c = 0, most = 0;
+  for (int k = 1; k <= kRingMaxCluster && (l.cap <= 0 || k <= l.cap); ++k) {
+    if (slots(k) < kMinSlots) continue;
+    const int n_ctas = k * clusters_that_fit<DT>(k, l);
+    if (n_ctas > most) {
+      most = n_ctas;
+      c = k;
+    }
+  }
+  if (c == 0) return false;
   while (2 * c <= kRingMaxCluster && v.rows * 2 * c <= static_cast<uint64_t>(l.sm_count) && n >= 2 * c * kMinChunks &&
          (l.cap <= 0 || 2 * c <= l.cap))
     c *= 2;
+  const int fit = clusters_that_fit<DT>(c, l);
+  if (fit == 0) return false;
   a.slots = slots(c);
   a.slot_bytes = static_cast<uint32_t>(slot_bytes(c));
-  int& fit = l.ring_clusters[(DT == kBF16 ? 1 : 0) * (kRingMaxCluster + 1) + c];
-  if (fit == 0) {
-    // asked once a group, with the most shared memory: one CTA to an SM
-    if (cudaFuncSetAttribute(distill_ring_kernel<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(l.smem_optin)) != cudaSuccess ||
-        ask_clusters<DT>(c, l.smem_optin, &fit) != cudaSuccess || fit <= 0) {
-      fit = 0;
-      cudaGetLastError();
-      return false;
-    }
-  }
   l.cluster = c;
   l.clusters = fit;
   if (l.cap > 0 && l.clusters * c > l.cap) l.clusters = l.cap / c;

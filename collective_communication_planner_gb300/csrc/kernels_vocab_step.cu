@@ -17,8 +17,7 @@ constexpr int kStepCtasPerSm = 5;
 template <int DT>
 __global__ void __launch_bounds__(kThreads, kStepCtasPerSm) distill_step_kernel(const __grid_constant__ DistillArgs a) {
   __shared__ GradSegments seg;
-  __shared__ Named named;
-  __shared__ LossSlots loss;
+  __shared__ Entries named;
   __shared__ JoinSlots slots;
   const VocabArgs& v = a.v;
   const uint32_t ctas = cluster_size(), cta = cluster_rank();
@@ -36,14 +35,15 @@ __global__ void __launch_bounds__(kThreads, kStepCtasPerSm) distill_step_kernel(
       const TeacherRow q = read_teacher(a, t);
       uint32_t x[kMaxTop / 32];
       load_named<DT>(v, t, q, x);
-      keep_named<DT>(v, t, q, x, a.top_k, named, lo, hi, cta == 0);
-      if (cta == 0) set_loss<DT>(q, x, loss);
+      set_entries<DT>(q, x, a.top_k, named, [&](uint32_t column) {
+        return has_column<DT>(v, t, column, lo, hi, cta == 0);
+      });
     }
     Part p = scan_row<DT, false, true>(v, seg, lo, hi, cta == 0, KeepLoad(), [](float) {});
     p = row_join(p, c, slots, phase, ctas);
     const bool fast = fabsf(p.m) < -kClamp;
     const Stats st = fast ? stats_of(p, c) : slow_stats<DT>(v, seg, lo, hi, slots, phase, cta, ctas);
-    if (cta == 0 && threadIdx.x < 32) store_loss(a, t, loss, st);
+    if (cta == 0 && threadIdx.x < 32) store_loss(a, t, named, st);
     const float w = a.weights[t] * v.inv_temp;
     RowGrad g;
     g.set(v, st.max, st.log2_s, w * named.total, 0.f);
@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(kThreads, kStepCtasPerSm) distill_step_kernel(
     store_edges<DT>(v, seg, g, t, cta, ctas);
     if (!g.zero) {
       __syncthreads();
-      store_named<DT>(v, t, named, g, w, threadIdx.x);
+      if (threadIdx.x < named.count) store_named<DT>(v, t, named, g, w, threadIdx.x);
     }
   }
 }
@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kThreads, kStepCtasPerSm) distill_step_kernel(
 template <int DT>
 int launch_step_t(DistillArgs& a, VocabLaunch& l) {
   VocabArgs& v = a.v;
-  set_cut<DT>(v, 2);
+  set_cut<DT>(v, v.together ? 0 : 2);
   // CTAs of a row: few enough rows at once for L2 to keep them between the two
   // reads, or as many as the SMs take of few rows; every warp gets a chunk
   const uint64_t row_bytes = static_cast<uint64_t>(v.vocab) * Elem<DT>::kBytes;

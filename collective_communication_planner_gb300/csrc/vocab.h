@@ -37,6 +37,7 @@ struct VocabArgs {
   int used;         // ranks that hold valid columns
   uint32_t parts;   // gradients apart: work items of a row
   int aligned;      // every row of every buffer starts on a 16-byte boundary
+  int together;     // gradients: every row is as far from one as its logits are
   float inv_temp;   // 1 / temperature
   float exp2_scale; // log2(e) / temperature
   VocabCut cut;

@@ -625,22 +625,17 @@ __device__ __forceinline__ TeacherRow read_teacher(const DistillArgs& a, uint64_
   return teacher_row(a, load_teacher(a, t));
 }
 
-// What the loss needs of the entries, in shared memory: warp 0 writes it, with
-// the student's logits at the entries' columns, and reads it after the row's join.
-struct LossSlots {
+// A row's entries in shared memory: warp 0 (or the row's teacher warp) writes
+// them, with the student's logits at their columns.
+struct Entries {
   float q[kMaxTop], log_q[kMaxTop], x[kMaxTop];
+  // those whose column's gradient is this CTA's to write, in entry order: the
+  // column and the entry; columns are looked through four at a time, to a -1
+  alignas(16) int32_t column[kMaxTop];
+  uint8_t entry[kMaxTop];
+  int count;
+  float total;
 };
-
-template <int DT>
-__device__ __forceinline__ void set_loss(const TeacherRow& r, const uint32_t (&x)[kMaxTop / 32], LossSlots& l) {
-#pragma unroll
-  for (int i = 0; i < kMaxTop / 32; ++i) {
-    const int k = 32 * i + (threadIdx.x & 31);
-    l.q[k] = r.q[i];
-    l.log_q[k] = r.log_q[i];
-    l.x[k] = of_bits<DT>(x[i]);
-  }
-}
 
 // The bits of the student's logits at the entries' columns, all loads issued
 // together; of_bits when they are used.
@@ -658,13 +653,43 @@ __device__ __forceinline__ void load_named(const VocabArgs& v, uint64_t t, const
   }
 }
 
-// Warp 0: writes sum_k q_k (log q_k - log p_k) and the statistics of row t.
-__device__ __forceinline__ void store_loss(const DistillArgs& a, uint64_t t, const LossSlots& l, const Stats& st) {
+// `mine(column)`: whether its gradient is this CTA's to write
+template <int DT, typename F>
+__device__ __forceinline__ void set_entries(const TeacherRow& r, const uint32_t (&x)[kMaxTop / 32], int top_k,
+                                            Entries& e, F mine) {
+  const int lane = threadIdx.x & 31;
+  int count = 0;
+#pragma unroll
+  for (int i = 0; i < kMaxTop / 32; ++i) {
+    if (32 * i >= top_k) break;
+    const int k = 32 * i + lane;
+    e.q[k] = r.q[i];
+    e.log_q[k] = r.log_q[i];
+    e.x[k] = of_bits<DT>(x[i]);
+    const bool here = r.column[i] >= 0 && mine(static_cast<uint32_t>(r.column[i]));
+    const uint32_t mask = __ballot_sync(0xFFFFFFFFu, here);
+    if (here) {
+      const int at = count + __popc(mask & ((1u << lane) - 1));
+      e.column[at] = r.column[i];
+      e.entry[at] = static_cast<uint8_t>(k);
+    }
+    count += __popc(mask);
+  }
+  if (lane < 3 && count + lane < kMaxTop) e.column[count + lane] = -1;
+  if (lane == 0) {
+    e.count = count;
+    e.total = r.total;
+  }
+}
+
+// One warp: writes sum_k q_k (log q_k - log p_k) and the statistics of row t.
+__device__ __forceinline__ void store_loss(const DistillArgs& a, uint64_t t, const Entries& e, const Stats& st) {
   float loss = 0.f;
 #pragma unroll
   for (int i = 0; i < kMaxTop / 32; ++i) {
+    if (32 * i >= a.top_k) break;
     const int k = 32 * i + (threadIdx.x & 31);
-    if (!(l.q[k] <= 0.f)) loss += l.q[k] * (l.log_q[k] - st.log_prob(l.x[k], a.v.inv_temp));
+    if (!(e.q[k] <= 0.f)) loss += e.q[k] * (e.log_q[k] - st.log_prob(e.x[k], a.v.inv_temp));
   }
   for (int o = 16; o > 0; o >>= 1) loss += __shfl_xor_sync(0xFFFFFFFFu, loss, o);
   if ((threadIdx.x & 31) == 0) {

@@ -9,9 +9,9 @@ namespace vocab {
 
 // The segments of the current row for a gradient: where the logits and the
 // gradient start, and the first element of the body, which starts on a 16-byte
-// boundary of the gradient. Where the logits do not, a vector is put together
-// from two aligned ones, and the body leaves both ends of the segment enough
-// elements that those lie within it.
+// boundary of the gradient. Where the logits do not (v.together is not set), a
+// vector is put together from two aligned ones, and the body leaves both ends of
+// the segment enough elements that those lie within it.
 struct GradSegments : Segments {
   char* dst[kMaxRanks];
   template <int DT>
@@ -21,8 +21,10 @@ struct GradSegments : Segments {
 };
 
 template <int DT>
-__device__ __forceinline__ uint32_t head_of(const char* dst) {
-  return static_cast<uint32_t>(-reinterpret_cast<uintptr_t>(dst) & 15) / Elem<DT>::kBytes + Elem<DT>::kVec;
+__device__ __forceinline__ uint32_t head_of(const VocabArgs& v, const char* dst) {
+  if (v.aligned) return 0;
+  const uint32_t gap = static_cast<uint32_t>(-reinterpret_cast<uintptr_t>(dst) & 15) / Elem<DT>::kBytes;
+  return v.together ? gap : gap + Elem<DT>::kVec;
 }
 
 template <int DT>
@@ -30,7 +32,7 @@ __device__ __forceinline__ void set_segment(const VocabArgs& v, uint64_t t, uint
   s.src[r] = static_cast<const char*>(v.p.src[r]) + t * v.src_stride * Elem<DT>::kBytes;
   char* dst = static_cast<char*>(v.p.dst[r]) + t * v.dst_stride * Elem<DT>::kBytes;
   s.dst[r] = dst;
-  s.head[r] = v.aligned ? 0 : head_of<DT>(dst);
+  s.head[r] = head_of<DT>(v, dst);
 }
 
 // thread r < used sets rank r's segment of row t; the caller synchronises
@@ -173,7 +175,7 @@ template <int DT>
 __device__ __forceinline__ uint32_t chunk_of(const VocabArgs& v, uint64_t t, uint32_t column) {
   const uint32_t seg = column / v.shard, col = column - seg * v.shard;
   const char* dst = static_cast<const char*>(v.p.dst[seg]) + t * v.dst_stride * Elem<DT>::kBytes;
-  const uint32_t head = v.aligned ? 0 : head_of<DT>(dst);
+  const uint32_t head = head_of<DT>(v, dst);
   const uint32_t vectors = seg + 1 == v.used ? v.cut.last : v.cut.full, vec = (col - head) / Elem<DT>::kVec;
   if (col < head || vec >= vectors) return kEdge;
   return seg * v.cut.per_segment + vec / kChunkVectors;
@@ -194,64 +196,26 @@ __device__ __forceinline__ void write_column(const VocabArgs& v, uint64_t t, uin
   store_one<DT>(static_cast<char*>(v.p.dst[seg]) + (t * v.dst_stride + column - seg * v.shard) * Elem<DT>::kBytes, y);
 }
 
-// The teacher's columns that fall to this CTA, in entry order: after the
-// body's stores those columns get their own value.
-struct Named {
-  alignas(16) int32_t column[kMaxTop];
-  float q[kMaxTop], x[kMaxTop];
-  float total;
-  int count;
-};
-
-// Warp 0 keeps the entries of the row whose column is in chunks [lo, hi), or,
-// with `edges`, an edge element, in entry order, with the logits there, since an
-// in-place gradient replaces them.
+// The own term of the i-th of the entries whose columns are this CTA's, after a
+// barrier behind the body's stores. The logit there is the entry's, read before
+// an in-place gradient replaced it.
 template <int DT>
-__device__ __forceinline__ void keep_named(const VocabArgs& v, uint64_t t, const TeacherRow& r,
-                                           const uint32_t (&x)[kMaxTop / 32], int top_k, Named& n, uint32_t lo,
-                                           uint32_t hi, bool edges) {
-  int count = 0;
-#pragma unroll
-  for (int i = 0; i < kMaxTop / 32; ++i) {
-    if (32 * i >= top_k) break;
-    const bool here = r.column[i] >= 0 && has_column<DT>(v, t, r.column[i], lo, hi, edges);
-    const uint32_t mask = __ballot_sync(0xFFFFFFFFu, here);
-    if (here) {
-      const int at = count + __popc(mask & ((1u << (threadIdx.x & 31)) - 1));
-      n.column[at] = r.column[i];
-      n.q[at] = r.q[i];
-      n.x[at] = of_bits<DT>(x[i]);
-    }
-    count += __popc(mask);
-  }
-  // columns are looked through four at a time
-  if ((threadIdx.x & 31) < 3 && count + (threadIdx.x & 31) < kMaxTop) n.column[count + (threadIdx.x & 31)] = -1;
-  if ((threadIdx.x & 31) == 0) {
-    n.count = count;
-    n.total = r.total;
-  }
-}
-
-// after a barrier behind the body's stores
-template <int DT>
-__device__ __forceinline__ void store_named(const VocabArgs& v, uint64_t t, const Named& n, const RowGrad& g, float weight,
-                                            int i) {
-  if (i >= n.count) return;
-  const int32_t column = n.column[i];
+__device__ __forceinline__ void store_named(const VocabArgs& v, uint64_t t, const Entries& e, const RowGrad& g,
+                                            float weight, int i) {
+  const int32_t column = e.column[i];
   float q = 0.f;
   bool first = true;  // or an earlier entry names it too and does this
-  for (int j = 0; j < n.count; j += 4) {
-    const int4 c = *reinterpret_cast<const int4*>(&n.column[j]);
+  for (int j = 0; j < e.count; j += 4) {
+    const int4 c = *reinterpret_cast<const int4*>(&e.column[j]);
     const int32_t four[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       if (four[k] == column) {
         first = first && j + k >= i;
-        q += n.q[j + k];
+        q += e.q[e.entry[j + k]];
       }
   }
-  if (!first) return;
-  write_column<DT>(v, t, column, g.one(n.x[i]) - q * weight);
+  if (first) write_column<DT>(v, t, column, g.one(e.x[e.entry[i]]) - q * weight);
 }
 
 }  // namespace vocab

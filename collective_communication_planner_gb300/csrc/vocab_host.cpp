@@ -105,6 +105,9 @@ bool fill(tcclGroup* g, const void* const* logits, const tcclVocab_t* shape, voi
     return ok;
   };
   v->aligned = whole(shape->row_stride, const_cast<void* const*>(logits)) && (!grads || whole(grad_stride, grads));
+  v->together = grads != nullptr && ((shape->row_stride - grad_stride) * es % 16 == 0 || shape->rows == 1);
+  for (int r = 0; grads && r < g->nranks; ++r)
+    v->together = v->together && ((uintptr_t)logits[r] - (uintptr_t)grads[r]) % 16 == 0;
   v->rows = shape->rows;
   v->src_stride = shape->row_stride;
   v->dst_stride = grad_stride;
