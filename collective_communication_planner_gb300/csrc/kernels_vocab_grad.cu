@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(kThreads, 5) log_probs_grad_kernel(const __gri
     const bool named = threadIdx.x == 0 && !g.zero && has_column<DT>(v, t, column, it.lo, it.hi, it.part == 0);
     const float x = named ? read_column<DT>(v, t, column) : 0.f;
     __syncthreads();
-    if (g.zero) zero_chunks<DT>(v, seg, it.lo, it.hi, threadIdx.x >> 5, v.step);
+    if (g.zero) zero_chunks<DT>(v, seg, first_chunk(v, it.lo, it.hi), it.hi, v.step);
     else store_chunks<DT, SLOPE>(v, seg, g, it.lo, it.hi);
     store_edges<DT>(v, seg, g, t, it.part, v.parts);
     __syncthreads();
@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kThreads, 5) distill_grad_kernel(const __grid_
     RowGrad g;
     g.set(v, m, ls * kLog2e, w * named.total, 0.f);
     g.zero = zero;
-    if (zero) zero_chunks<DT>(v, seg, it.lo, it.hi, threadIdx.x >> 5, v.step);
+    if (zero) zero_chunks<DT>(v, seg, first_chunk(v, it.lo, it.hi), it.hi, v.step);
     else store_chunks<DT, false>(v, seg, g, it.lo, it.hi);
     store_edges<DT>(v, seg, g, t, it.part, v.parts);
     if (!zero) {

@@ -25,7 +25,13 @@ constexpr uint32_t kSumWarps = 8, kGradWarps = 8;
 constexpr uint32_t kTeacherWarps = 3;  // they take the rows in turn
 constexpr uint32_t kLoaderWarp = kSumWarps + kGradWarps, kFirstTeacher = kLoaderWarp + 1;
 constexpr int kThreads = (kFirstTeacher + kTeacherWarps) * 32;
-constexpr uint32_t kMinChunks = 16;  // a CTA's slice: 32 KiB
+// Rows that the ring takes: long ones, since a row's joins and barriers take it
+// about 3 us whatever its bytes (GB300, 4096 rows bf16: 16384 columns 78 us,
+// the kernel that reads twice 63; 32768: 99 and 101; 65536: 175 and 212), several
+// to a cluster (64 rows of 131072: 11.7 and 11.0 us), and not of many short odd
+// segments, whose edge elements one warp does (512 x 50257 over 16 ranks: 47
+// and 23 us).
+constexpr uint32_t kMinChunks = 32, kMinRowsPerCluster = 4, kMaxEdges = 128;
 constexpr int kMinSlots = 3, kMaxSlots = 4;
 // What goes with a row within the CTA, row n's being set n % kSets. A teacher
 // warp sets row n + 3's up before it is done with row n, and row n + 6's after
@@ -42,6 +48,18 @@ constexpr uint32_t kParts = kSumWarps + 1;
 constexpr uint32_t kJoins = 9;
 static_assert(kJoins > 2 * kMaxSlots && kJoins > kMaxSlots + kTeacherWarps, "parts overwritten while they may be read");
 
+// Where the segments of a slot's row go: the gradient's first element, how many
+// come before the body, and how far the body's logits are from a granule.
+struct RingSegments {
+  char* dst[kMaxRanks];
+  uint32_t head[kMaxRanks];
+  uint8_t off[kMaxRanks];
+  template <int DT>
+  __device__ __forceinline__ char* to(uint32_t seg, uint32_t col) const {
+    return dst[seg] + static_cast<uint64_t>(col) * Elem<DT>::kBytes;
+  }
+};
+
 struct RingShared {
   uint64_t full[kMaxSlots];   // a slot's copies have landed (bytes)
   uint64_t empty[kMaxSlots];  // every gradient warp is done with a slot's row
@@ -50,7 +68,7 @@ struct RingShared {
                               // teacher warps' arrivals, the other sum warps' bytes
   uint64_t never;             // test hook
   float2 part[kJoins][kRingMaxCluster * kParts];  // maximum and sum
-  GradSegments seg[kMaxSlots];
+  RingSegments seg[kMaxSlots];
   Entries named[kSets];
   float weight[kSets];
   int abort;
@@ -141,15 +159,9 @@ __device__ __forceinline__ void load_slot(const char* chunk, uint32_t m, const C
   else load_vectors<DT>(at + m, w.vector(), end, x, [](const char* p) { return load_any(p, SharedLoad()); });
 }
 
-// how far the logits of a segment's body are from a 16-byte boundary
-template <int DT>
-__device__ __forceinline__ uint32_t off_granule(const GradSegments& s, uint32_t seg) {
-  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(s.at<DT>(seg, s.head[seg])) & 15);
-}
-
 // A warp's part of the slice in a slot.
 template <int DT>
-__device__ __forceinline__ Part slot_part(const VocabArgs& v, const GradSegments& s, const char* slot,
+__device__ __forceinline__ Part slot_part(const VocabArgs& v, const RingSegments& s, const char* slot,
                                           uint32_t lo, uint32_t hi, uint32_t warp, const ChunkStep& step) {
   const float c = v.exp2_scale;
   const uint32_t seg0 = lo / v.cut.per_segment;
@@ -157,7 +169,7 @@ __device__ __forceinline__ Part slot_part(const VocabArgs& v, const GradSegments
   f32x2 sum[4] = {0, 0, 0, 0};
   for (ChunkWalk w(v.cut, lo + warp); w.index < hi; w.next(v.cut, step)) {
     Vec<DT> x[kBatch];
-    load_slot<DT>(slot_chunk(slot, w, lo, seg0), off_granule<DT>(s, w.seg), w, w.vectors(v), x);
+    load_slot<DT>(slot_chunk(slot, w, lo, seg0), s.off[w.seg], w, w.vectors(v), x);
     const float top = fmaxf(p.m, batch_max<DT, kBatch>(x));
     // a first maximum finds sums of 0; the same maximum, -inf among them, changes nothing
     const float f = top == p.m ? 1.f : exp2_ftz((p.m - top) * c);
@@ -181,13 +193,13 @@ __device__ __forceinline__ Part slot_part(const VocabArgs& v, const GradSegments
 
 // The gradient of a warp's chunks of the slice in a slot.
 template <int DT, bool FAST>
-__device__ __forceinline__ void store_slot(const VocabArgs& v, const GradSegments& s, const RowGrad& g,
+__device__ __forceinline__ void store_slot(const VocabArgs& v, const RingSegments& s, const RowGrad& g,
                                            const char* slot, uint32_t lo, uint32_t hi, uint32_t warp, const ChunkStep& step) {
   const uint32_t seg0 = lo / v.cut.per_segment;
   for (ChunkWalk w(v.cut, lo + warp); w.index < hi; w.next(v.cut, step)) {
     Vec<DT> x[kBatch];
     const uint32_t first = w.vector(), end = w.vectors(v);
-    load_slot<DT>(slot_chunk(slot, w, lo, seg0), off_granule<DT>(s, w.seg), w, end, x);
+    load_slot<DT>(slot_chunk(slot, w, lo, seg0), s.off[w.seg], w, end, x);
     store_chunk<DT, false, FAST>(g, x, s.to<DT>(w.seg, s.head[w.seg]) + static_cast<uint64_t>(first) * 16, first, end);
   }
 }
@@ -277,9 +289,9 @@ __device__ void grad_warp(const DistillArgs& a, RingShared& s, const unsigned ch
     if (!wait(&s.full[slot], n / a.slots)) return;  // long done; makes the copies visible to this warp
     const Stats st = row_parts(s, n, ctas, v.exp2_scale);
     const float w = s.weight[n % kSets], total = s.named[n % kSets].total;
-    const GradSegments& seg = s.seg[slot];
+    const RingSegments& seg = s.seg[slot];
     if (w == 0.f || total == 0.f || st.empty()) {
-      zero_chunks<DT>(v, seg, lo, hi, warp, a.grad_step);
+      zero_chunks<DT>(v, seg, lo + warp, hi, a.grad_step);
     } else {
       RowGrad g;
       g.set(v, st.max, st.log2_s, w * total, 0.f);
@@ -309,8 +321,16 @@ __device__ __forceinline__ void fill_slot(const DistillArgs& a, RingShared& s, u
                                           uint32_t n, const Piece (&piece)[kMaxRanks / 32]) {
   const VocabArgs& v = a.v;
   const uint32_t slot = n % a.slots, lane = threadIdx.x & 31;
-  GradSegments& seg = s.seg[slot];
-  for (uint32_t r = lane; r < v.used; r += 32) set_segment<DT>(v, rows.row(n), r, seg);
+  RingSegments& seg = s.seg[slot];
+  const uint64_t t = rows.row(n);
+  const auto body = [&](uint32_t r) {
+    return static_cast<const char*>(v.p.src[r]) + (t * v.src_stride + seg.head[r]) * Elem<DT>::kBytes;
+  };
+  for (uint32_t r = lane; r < v.used; r += 32) {
+    seg.dst[r] = static_cast<char*>(v.p.dst[r]) + t * v.dst_stride * Elem<DT>::kBytes;
+    seg.head[r] = head_of<DT>(v, seg.dst[r]);
+    seg.off[r] = static_cast<uint8_t>(reinterpret_cast<uintptr_t>(body(r)) & 15);
+  }
   __syncwarp();
   uint32_t total = 0, bytes[kMaxRanks / 32];
   const char* from[kMaxRanks / 32];
@@ -319,9 +339,9 @@ __device__ __forceinline__ void fill_slot(const DistillArgs& a, RingShared& s, u
     const Piece& p = piece[i];
     bytes[i] = 0;
     if (p.vectors == 0) continue;
-    const uint32_t off = off_granule<DT>(seg, p.seg);
+    const uint32_t off = seg.off[p.seg];
     bytes[i] = (p.vectors + (off ? 1 : 0)) * 16;  // whole granules
-    from[i] = seg.at<DT>(p.seg, seg.head[p.seg]) - off + static_cast<uint64_t>(p.begin) * 16;
+    from[i] = body(p.seg) - off + static_cast<uint64_t>(p.begin) * 16;
     total += bytes[i];
   }
   total = __reduce_add_sync(0xFFFFFFFFu, total);
@@ -547,10 +567,7 @@ bool plan_t(DistillArgs& a, VocabLaunch& l) {
   VocabArgs& v = a.v;
   set_cut<DT>(v, v.together ? 0 : 2);
   const uint32_t n = v.cut.chunks;
-  // short rows: a row's latency (about 3 us of joins and barriers) is not
-  // covered by its bytes, and the kernel that reads twice has more rows in flight
-  if (n < kMinChunks) return false;
-  if (l.smem_optin < kSharedBytes) return false;
+  if (n < kMinChunks || v.cut.edges > kMaxEdges || l.smem_optin < kSharedBytes) return false;
   const size_t room = l.smem_optin - kSharedBytes;
   const auto slot_bytes = [&](int c) { return static_cast<size_t>((n + c - 1) / c) * (kChunkVectors * 16) + v.used * 16; };
   const auto slots = [&](int c) {
@@ -558,8 +575,7 @@ bool plan_t(DistillArgs& a, VocabLaunch& l) {
   };
   // Of the clusters whose slots hold three slices, the one that leaves the
   // fewest SMs without a CTA (GB300, one CTA to an SM: clusters of 1 to 8 fill
-  // 152, 152, 138, 144, 140, 138, 105, 120 of 152). Fewer rows than clusters:
-  // larger ones instead.
+  // 152, 152, 138, 144, 140, 138, 105, 120 of 152).
   int c = 0, most = 0;
   for (int k = 1; k <= kRingMaxCluster && (l.cap <= 0 || k <= l.cap); ++k) {
     if (slots(k) < kMinSlots) continue;
@@ -570,17 +586,12 @@ bool plan_t(DistillArgs& a, VocabLaunch& l) {
     }
   }
   if (c == 0) return false;
-  while (2 * c <= kRingMaxCluster && v.rows * 2 * c <= static_cast<uint64_t>(l.sm_count) && n >= 2 * c * kMinChunks &&
-         (l.cap <= 0 || 2 * c <= l.cap))
-    c *= 2;
-  const int fit = clusters_that_fit<DT>(c, l);
-  if (fit == 0) return false;
+  l.cluster = c;
+  l.clusters = clusters_that_fit<DT>(c, l);
+  if (l.cap > 0 && l.clusters * c > l.cap) l.clusters = l.cap / c;
+  if (v.rows < static_cast<uint64_t>(l.clusters) * kMinRowsPerCluster) return false;
   a.slots = slots(c);
   a.slot_bytes = static_cast<uint32_t>(slot_bytes(c));
-  l.cluster = c;
-  l.clusters = fit;
-  if (l.cap > 0 && l.clusters * c > l.cap) l.clusters = l.cap / c;
-  if (v.rows < static_cast<uint64_t>(l.clusters)) l.clusters = static_cast<int>(v.rows);
   return true;
 }
 

@@ -6,10 +6,11 @@ namespace {
 
 using namespace vocab;
 
-constexpr int kThreads = 256;
+constexpr int kWarps = 8;                    // that stream; one more reads the teacher's entries
+constexpr int kThreads = (kWarps + 1) * 32;
 constexpr uint64_t kKeepBytes = 52ull << 20;  // rows that L2 keeps between two reads
 constexpr int kStepCluster = 8;
-constexpr int kStepCtasPerSm = 5;
+constexpr int kStepCtasPerSm = 4;
 
 // Loss and gradient in one call: a cluster of CTAs sums up a row, joins its
 // statistics through distributed shared memory and reads it again, from L2,
@@ -31,7 +32,8 @@ __global__ void __launch_bounds__(kThreads, kStepCtasPerSm) distill_step_kernel(
     __syncthreads();  // the last row's segments and columns are done with
     set_segments<DT>(v, t, seg);
     __syncthreads();
-    if (threadIdx.x < 32) {
+    const float w = a.weights[t] * v.inv_temp;
+    if (threadIdx.x >= kWarps * 32) {
       const TeacherRow q = read_teacher(a, t);
       uint32_t x[kMaxTop / 32];
       load_named<DT>(v, t, q, x);
@@ -43,14 +45,13 @@ __global__ void __launch_bounds__(kThreads, kStepCtasPerSm) distill_step_kernel(
     p = row_join(p, c, slots, phase, ctas);
     const bool fast = fabsf(p.m) < -kClamp;
     const Stats st = fast ? stats_of(p, c) : slow_stats<DT>(v, seg, lo, hi, slots, phase, cta, ctas);
-    if (cta == 0 && threadIdx.x < 32) store_loss(a, t, named, st);
-    const float w = a.weights[t] * v.inv_temp;
+    if (cta == 0 && threadIdx.x >= kWarps * 32) store_loss(a, t, named, st);
     RowGrad g;
     g.set(v, st.max, st.log2_s, w * named.total, 0.f);
     g.zero = w == 0.f || named.total == 0.f || st.empty();
     // An in-place gradient may be written from here on: past the join's
     // barrier a CTA reads its own columns only, each before it replaces it.
-    if (g.zero) zero_chunks<DT>(v, seg, lo, hi, threadIdx.x >> 5, v.step);
+    if (g.zero) zero_chunks<DT>(v, seg, first_chunk(v, lo, hi), hi, v.step);
     else store_chunks<DT, false>(v, seg, g, lo, hi);
     store_edges<DT>(v, seg, g, t, cta, ctas);
     if (!g.zero) {
@@ -70,13 +71,13 @@ int launch_step_t(DistillArgs& a, VocabLaunch& l) {
   const uint64_t resident = static_cast<uint64_t>(l.sm_count) * kStepCtasPerSm;
   const auto kept = [&](int c) { return (v.rows < resident / c ? v.rows : resident / c) * row_bytes; };
   int c = 1;
-  while (c < kStepCluster && v.cut.chunks >= static_cast<uint32_t>(2 * c * kThreads / 32) &&
+  while (c < kStepCluster && v.cut.chunks >= static_cast<uint32_t>(2 * c * kWarps) &&
          (l.cap <= 0 || 2 * c <= l.cap) && (v.rows * 2 * c <= resident || kept(c) > kKeepBytes))
     c *= 2;
   uint64_t rows = v.rows;
   if (l.cap > 0 && rows * c > static_cast<uint64_t>(l.cap)) rows = l.cap / c;
   const uint64_t most = static_cast<uint64_t>(1) << 27;
-  return launch_rows(distill_step_kernel<DT>, a, l, (rows < most ? rows : most) * c, kThreads, c, 0);
+  return launch_rows(distill_step_kernel<DT>, a, l, (rows < most ? rows : most) * c, kThreads, c, 0, kWarps);
 }
 
 }  // namespace

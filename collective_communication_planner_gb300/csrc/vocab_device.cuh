@@ -381,6 +381,17 @@ __device__ __forceinline__ void load_chunk(const VocabArgs& v, const char* body,
   else load_vectors<DT>(at, first, end, x, [&](const char* p) { return load_any(p, load); });
 }
 
+// The warps that stream are the first v.step.warps of the CTA: a warp's first
+// chunk of [lo, hi), and a thread's first edge element and the step to its next.
+__device__ __forceinline__ uint32_t first_chunk(const VocabArgs& v, uint32_t lo, uint32_t hi) {
+  const uint32_t warp = threadIdx.x >> 5;
+  return warp < v.step.warps ? lo + warp : hi;
+}
+__device__ __forceinline__ uint32_t first_edge(const VocabArgs& v, bool edges) {
+  return edges && threadIdx.x < v.step.warps * 32 ? threadIdx.x : v.cut.edges;
+}
+__device__ __forceinline__ uint32_t next_edge(const VocabArgs& v) { return v.step.warps * 32; }
+
 // segment of edge element `e` of a row, and its column there
 template <int DT>
 __device__ __forceinline__ void edge_at(const VocabArgs& v, const Segments& s, uint32_t e, uint32_t& seg,
@@ -400,7 +411,7 @@ __device__ __forceinline__ void edge_at(const VocabArgs& v, const Segments& s, u
 template <int DT, typename F>
 __device__ __forceinline__ void each_element(const VocabArgs& v, const Segments& s, uint32_t lo, uint32_t hi,
                                              bool edges, F f) {
-  for (ChunkWalk w(v.cut, lo + (threadIdx.x >> 5)); w.index < hi; w.next(v.cut, v.step)) {
+  for (ChunkWalk w(v.cut, first_chunk(v, lo, hi)); w.index < hi; w.next(v.cut, v.step)) {
     Vec<DT> x[kBatch];
     load_chunk<DT, true>(v, s.at<DT>(w.seg, s.head[w.seg]), w, x, StreamLoad());
 #pragma unroll
@@ -409,7 +420,7 @@ __device__ __forceinline__ void each_element(const VocabArgs& v, const Segments&
 #pragma unroll
         for (int i = 0; i < Elem<DT>::kVec; ++i) f(x[k].get(i));
   }
-  for (uint32_t e = threadIdx.x; edges && e < v.cut.edges; e += blockDim.x) {
+  for (uint32_t e = first_edge(v, edges); e < v.cut.edges; e += next_edge(v)) {
     uint32_t seg, col;
     edge_at<DT>(v, s, e, seg, col);
     f(load_one<DT>(s.at<DT>(seg, col)));
@@ -520,7 +531,7 @@ __device__ __forceinline__ Part scan_row(const VocabArgs& v, const Segments& seg
   Part a{kClamp, 0.f, 0.f};
   float r = __fmul_rn(kClamp, c);
   f32x2 s[2] = {0, 0}, u[2] = {0, 0};
-  for (ChunkWalk w(v.cut, lo + (threadIdx.x >> 5)); w.index < hi; w.next(v.cut, v.step)) {
+  for (ChunkWalk w(v.cut, first_chunk(v, lo, hi)); w.index < hi; w.next(v.cut, v.step)) {
     Vec<DT> x[kBatch];
     load_chunk<DT, ANY>(v, seg.at<DT>(w.seg, seg.head[w.seg]), w, x, load_vector);
     top_of(add_chunk<DT, ENTROPY>(a, r, s, u, x, c));
@@ -532,7 +543,7 @@ __device__ __forceinline__ Part scan_row(const VocabArgs& v, const Segments& seg
   unpack(u[0], s0, s1);
   unpack(u[1], s2, s3);
   a.u = (s0 + s1) + (s2 + s3);
-  for (uint32_t e = threadIdx.x; edges && e < v.cut.edges; e += blockDim.x) {
+  for (uint32_t e = first_edge(v, edges); e < v.cut.edges; e += next_edge(v)) {
     uint32_t es, col;
     edge_at<DT>(v, seg, e, es, col);
     const float x = max_f32(load_one<DT>(seg.at<DT>(es, col)), kClamp);
@@ -630,7 +641,7 @@ __device__ __forceinline__ TeacherRow read_teacher(const DistillArgs& a, uint64_
 struct Entries {
   float q[kMaxTop], log_q[kMaxTop], x[kMaxTop];
   // those whose column's gradient is this CTA's to write, in entry order: the
-  // column and the entry; columns are looked through four at a time, to a -1
+  // column and the entry
   alignas(16) int32_t column[kMaxTop];
   uint8_t entry[kMaxTop];
   int count;
@@ -675,7 +686,6 @@ __device__ __forceinline__ void set_entries(const TeacherRow& r, const uint32_t 
     }
     count += __popc(mask);
   }
-  if (lane < 3 && count + lane < kMaxTop) e.column[count + lane] = -1;
   if (lane == 0) {
     e.count = count;
     e.total = r.total;
@@ -732,12 +742,13 @@ int launch_distill_step(int dtype, DistillArgs& a, VocabLaunch& l);
 bool plan_distill_ring(int dtype, DistillArgs& a, VocabLaunch& l);
 int launch_distill_ring(int dtype, DistillArgs& a, VocabLaunch& l);
 
-// Launches `kernel` on clusters of `cluster` CTAs; uncapped calls start early
+// Launches `kernel` on clusters of `cluster` CTAs whose first `stream_warps`
+// warps stream (0: all); uncapped calls start early
 // (the kernel waits before it touches memory).
 template <typename Kernel, typename Args>
 inline int launch_rows(Kernel kernel, Args& a, VocabLaunch& l, uint64_t grid, int threads, int cluster,
-                       size_t smem) {
-  a.v.step = step_of(a.v.cut, threads / 32);
+                       size_t smem, int stream_warps = 0) {
+  a.v.step = step_of(a.v.cut, stream_warps ? stream_warps : threads / 32);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(static_cast<unsigned>(threads));

@@ -121,7 +121,7 @@ __device__ __forceinline__ void store_chunk(const RowGrad& g, Vec<DT> (&x)[kBatc
 template <int DT, bool SLOPE, bool FAST>
 __device__ __forceinline__ void store_chunks(const VocabArgs& v, const GradSegments& s, const RowGrad& g, uint32_t lo,
                                              uint32_t hi) {
-  for (ChunkWalk w(v.cut, lo + (threadIdx.x >> 5)); w.index < hi; w.next(v.cut, v.step)) {
+  for (ChunkWalk w(v.cut, first_chunk(v, lo, hi)); w.index < hi; w.next(v.cut, v.step)) {
     Vec<DT> x[kBatch];
     const uint32_t first = w.vector(), head = s.head[w.seg];
     load_chunk<DT, true>(v, s.at<DT>(w.seg, head), w, x, StreamLoad());
@@ -135,12 +135,13 @@ __device__ __forceinline__ void store_chunks(const VocabArgs& v, const GradSegme
   else store_chunks<DT, SLOPE, false>(v, s, g, lo, hi);
 }
 
-template <int DT>
-__device__ __forceinline__ void zero_chunks(const VocabArgs& v, const GradSegments& s, uint32_t lo, uint32_t hi,
-                                            uint32_t warp, const ChunkStep& step) {
-  for (ChunkWalk w(v.cut, lo + warp); w.index < hi; w.next(v.cut, step)) {
+// zeros for the chunks first, first + step, ... below hi
+template <int DT, typename S>
+__device__ __forceinline__ void zero_chunks(const VocabArgs& v, const S& s, uint32_t first_of, uint32_t hi,
+                                            const ChunkStep& step) {
+  for (ChunkWalk w(v.cut, first_of); w.index < hi; w.next(v.cut, step)) {
     const uint32_t first = w.vector(), end = w.vectors(v);
-    char* to = s.to<DT>(w.seg, s.head[w.seg]) + static_cast<uint64_t>(first) * 16;
+    char* to = s.template to<DT>(w.seg, s.head[w.seg]) + static_cast<uint64_t>(first) * 16;
 #pragma unroll
     for (int k = 0; k < kBatch; ++k)
       if (first + k * 32 < end) dev::st_global_v4(to + k * 512, make_uint4(0, 0, 0, 0));
@@ -161,7 +162,7 @@ __device__ __forceinline__ void zero_padding(const VocabArgs& v, uint64_t t, uin
 template <int DT>
 __device__ __forceinline__ void store_edges(const VocabArgs& v, const GradSegments& s, const RowGrad& g, uint64_t t,
                                             uint32_t cta, uint32_t ctas) {
-  for (uint32_t e = threadIdx.x; cta == 0 && e < v.cut.edges; e += blockDim.x) {
+  for (uint32_t e = first_edge(v, cta == 0); e < v.cut.edges; e += next_edge(v)) {
     uint32_t seg, col;
     edge_at<DT>(v, s, e, seg, col);
     store_one<DT>(s.to<DT>(seg, col), g.zero ? 0.f : g.one(load_one<DT>(s.at<DT>(seg, col))));
@@ -204,18 +205,21 @@ __device__ __forceinline__ void store_named(const VocabArgs& v, uint64_t t, cons
                                             float weight, int i) {
   const int32_t column = e.column[i];
   float q = 0.f;
-  bool first = true;  // or an earlier entry names it too and does this
-  for (int j = 0; j < e.count; j += 4) {
-    const int4 c = *reinterpret_cast<const int4*>(&e.column[j]);
-    const int32_t four[4] = {c.x, c.y, c.z, c.w};
+  for (int j = 0; j < e.count; j += 32) {
+    uint32_t same = 0;  // which of entries j .. j + 31 name the column too
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (four[k] == column) {
-        first = first && j + k >= i;
-        q += e.q[e.entry[j + k]];
-      }
+    for (int k = 0; k < 32; k += 4) {
+      const int4 c = *reinterpret_cast<const int4*>(&e.column[j + k]);
+      same |= (c.x == column) << k | (c.y == column) << (k + 1) | (c.z == column) << (k + 2) | (c.w == column) << (k + 3);
+    }
+    for (; same; same &= same - 1) {
+      const int k = j + __ffs(same) - 1;
+      if (k >= e.count) break;  // past the end: an earlier row's
+      if (k < i) return;        // an earlier entry does this
+      q += e.q[e.entry[k]];
+    }
   }
-  if (first) write_column<DT>(v, t, column, g.one(e.x[e.entry[i]]) - q * weight);
+  write_column<DT>(v, t, column, g.one(e.x[e.entry[i]]) - q * weight);
 }
 
 }  // namespace vocab

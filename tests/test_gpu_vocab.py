@@ -532,6 +532,107 @@ def test_caps_and_many_rows(groups, cap):
     check_log_probs(g, big, p, 24, rng.integers(0, 40, 3000), "bf16", k=2, cap=cap if cap > 3 else 0)
 
 
+RING_THREADS = 640  # the persistent kernel of long rows
+
+# ranks, shard, vocab, datatype, cap, rows: clusters of 1, 2, 4, 5 to 8 CTAs, one
+# of them or two, and rows enough for every slot and barrier to be used in turn
+RING = [(1, 33000, 33000, "bf16", 1, 29), (3, 11000, 32999, "bf16", 2, 61), (2, 24000, 48000, "f32", 4, 9),
+        (8, 16384, 131072, "bf16", 8, 23), (5, 20001, 100003, "f32", 8, 13), (2, 50001, 100002, "f32", 7, 11),
+        (4, 65536, 262144, "bf16", 8, 5)]
+
+
+@pytest.mark.parametrize("p,shard,vocab,dtype,cap,rows", RING)
+def test_long_rows(groups, p, shard, vocab, dtype, cap, rows):
+    """Rows that stay in shared memory between their sum and their gradient.
+    Under a cap few rows are enough for that kernel."""
+    rng = np.random.default_rng(vocab + rows)
+    x = make_logits(rng, rows, vocab, dtype)
+    lowest = torch.finfo(TORCH[dtype]).min
+    x[1] = float("-inf")
+    x[2, 10:] = float("-inf")
+    x[3] = lowest
+    x[4, : vocab // 2] = lowest
+    w = rng.normal(size=rows).astype(np.float32)
+    w[0] = 0.0
+    g = groups(p)
+    for k, temperature, known, kw in ((33, 1.0, False, {}), (128, 0.7, True, dict(gap=3, gap_out=1, offset=1, offset_out=2)),
+                                      (2, 2.0, False, dict(in_place=True, gap=1))):
+        ids, t = make_teacher(rng, rows, vocab, k)
+        ids[-1] = -1                       # no entries
+        ids[0, 0], ids[0, -1] = 0, vocab - 1
+        if k > 2:
+            ids[-2, 1::2] = ids[-2, 0]     # a column named many times
+        lse = (rng.normal(size=rows) + 4).astype(np.float32) if known else None
+        first = check_distill(g, x, p, shard, ids, t, dtype, temperature, lse, w, "bf16" if known else "f32",
+                              cap=cap, ways=("step",), **kw)
+        info = g.last_launch()
+        # many odd segments have too many edge elements for it
+        assert info["ctas"] <= cap and (info["threads"] == RING_THREADS) == (p <= 5 or "offset" not in kw), info
+        again = check_distill(g, x, p, shard, ids, t, dtype, temperature, lse, w, "bf16" if known else "f32",
+                              cap=cap, ways=("step",), **kw)
+        assert torch.equal(first[0][0], again[0][0])
+        assert all(torch.equal(m, n) for m, n in zip(first[0][2], again[0][2]))
+
+
+def test_long_rows_uncapped_and_special(groups):
+    """The same kernel over the whole device, with NaN and infinite logits, and
+    against the forward and the gradient apart."""
+    p, shard, vocab, rows, dtype = 4, 8192, 32768, 700, "bf16"
+    rng = np.random.default_rng(40)
+    x = make_logits(rng, rows, vocab, dtype)
+    x[5, 9000] = float("nan")
+    x[6, 3] = float("inf")
+    ids, t = make_teacher(rng, rows, vocab, 8)
+    w = np.abs(rng.normal(size=rows)).astype(np.float32) + 0.1
+    g = groups(p)
+    logits = cut(x, p, shard)
+    out = {}
+    for way in ("one", "two"):
+        loss, st, grads = f32(rows), f32(rows, 2), grad_buffers(x, p, shard, 0, 0)
+        if way == "one":
+            g.distill(logits, dev(ids, torch.int64), dev(t), loss, st, weights=dev(w), grads=grads)
+            assert g.last_launch()["threads"] == RING_THREADS
+        else:
+            g.distill(logits, dev(ids, torch.int64), dev(t), loss, st)
+            g.distill_backward(logits, dev(ids, torch.int64), dev(t), st, dev(w), grads)
+        torch.cuda.synchronize()
+        assert g.query_error() == tccl.tcclSuccess
+        out[way] = host(loss), glue(grads, vocab)[0]
+    bad = np.zeros(rows, bool)
+    bad[[5, 6]] = True
+    for loss, grad in out.values():
+        assert np.isnan(loss[bad]).all() and np.isfinite(loss[~bad]).all()
+        assert np.isnan(grad[bad]).all() and np.isfinite(grad[~bad]).all()
+    keep = ~bad
+    loss, tl, grad, tg = distill_bounds(x[torch.from_numpy(keep)], ids[keep], t[keep].astype(np.float32), 1.0, None, w[keep])
+    for got_loss, got in out.values():
+        close(got_loss[keep], loss, tl, "loss")
+        close_grad(got[keep], grad, tg, dtype, "gradient")
+
+
+def test_long_rows_wait_timeout(groups):
+    """A wait of the persistent kernel that runs out is reported, ends the
+    kernel, and leaves the next call right."""
+    p, shard, vocab, rows = 2, 65536, 131072, 12
+    rng = np.random.default_rng(41)
+    x = make_logits(rng, rows, vocab, "bf16")
+    ids, t = make_teacher(rng, rows, vocab, 4)
+    w = rng.normal(size=rows).astype(np.float32)
+    g = tccl.Group(p)
+    try:
+        g.set_config(wait_timeout_ms=30.0)
+        logits, grads, loss = cut(x, p, shard), grad_buffers(x, p, shard, 0, 0), f32(rows)
+        assert tccl.tcclGroupInjectWaitTimeout(g.handle, True, 2.0) == tccl.tcclSuccess
+        g.distill(logits, dev(ids, torch.int64), dev(t), loss, weights=dev(w), grads=grads, cta_cap=8)
+        assert g.last_launch()["threads"] == RING_THREADS
+        assert g.query_error() == tccl.tcclDeviceTimeout
+        assert tccl.tcclGroupInjectWaitTimeout(g.handle, False, 0.0) == tccl.tcclSuccess
+        check_distill(g, x, p, shard, ids, t, "bf16", w=w, cap=8, ways=("step",))
+        assert g.last_launch()["threads"] == RING_THREADS
+    finally:
+        g.close()
+
+
 def test_rows_far_apart(groups):
     """Element offsets past 2^32: the last row starts 4.4e9 elements in."""
     rng = np.random.default_rng(23)
