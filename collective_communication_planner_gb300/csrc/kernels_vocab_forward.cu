@@ -7,30 +7,45 @@ namespace {
 
 using namespace vocab;
 
-constexpr int kThreads = 256;
-constexpr int kMaxEntries = 64;    // stored chunk maxima per thread
-constexpr int kMaxWork = 512;      // of them looked at again for alternatives
+constexpr int kWarps = 8;          // of a CTA, but for short rows
+constexpr int kMaxEntries = 64;    // stored maxima of a thread
+constexpr int kMaxWork = 512;      // of a CTA's, looked at again for alternatives
 constexpr int kMaxCandidates = 1024;
 constexpr int kForwardCluster = 8;
 
-// The smallest bf16 number that is not below x, as its bits.
-__device__ __forceinline__ uint16_t bf16_above(float x) {
-  const uint32_t b = __float_as_uint(x);
-  return static_cast<uint16_t>((b & 0x80000000u) ? b >> 16 : (b + 0xFFFFu) >> 16);
+// Values as numbers in their order.
+__device__ __forceinline__ uint32_t order_of(float x) {
+  const uint32_t b = __float_as_uint(x + 0.f);  // -0 counts as 0
+  return (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
+__device__ __forceinline__ float order_value(uint32_t o) {
+  return __uint_as_float((o & 0x80000000u) ? o & 0x7FFFFFFFu : ~o);
+}
+// The upper half of a value's order: what is kept of maxima, and what the
+// threshold for alternatives is made of, so that comparing the halves says
+// whether a value reaches it.
+__device__ __forceinline__ uint32_t coarse_order(float x) { return order_of(x) >> 16; }
 
-// The statistics of a row over the cluster. With TOP, the maximum of every
-// 2^shift chunks is kept in `tops` for the alternatives, and thread_max set.
+// The statistics of a row over the cluster. With TOP, maxima are kept in `tops`
+// for the alternatives, of every 2^shift chunks a lane took or, with shift -2,
+// of each of its vectors; thread_max is set.
 template <int DT, bool ENTROPY, bool TOP>
 __device__ __forceinline__ Stats row_stats(const VocabArgs& v, const Segments& seg, uint32_t lo, uint32_t hi,
                                            uint32_t cta, uint32_t ctas, JoinSlots& slots, int& phase,
                                            uint16_t* tops, int shift, float& thread_max) {
   int chunk = 0;
   float entry = kClamp;
-  Part a = scan_row<DT, ENTROPY, false>(v, seg, lo, hi, cta == 0, StreamLoad(), [&](float top) {
+  Part a = scan_row<DT, ENTROPY, false>(v, seg, lo, hi, cta == 0, StreamLoad(), [&](float top, const Vec<DT>(&x)[kBatch]) {
     if (!TOP) return;
+    if (shift < 0) {
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        tops[(chunk * kBatch + k) * blockDim.x + threadIdx.x] = coarse_order(fmaxf(kClamp, vector_max(x[k])));
+      ++chunk;
+      return;
+    }
     entry = fmaxf(entry, top);
-    tops[(chunk >> shift) * kThreads + threadIdx.x] = bf16_above(entry);
+    tops[(chunk >> shift) * blockDim.x + threadIdx.x] = coarse_order(entry);
     if ((++chunk & ((1 << shift) - 1)) == 0) entry = kClamp;
   });
   thread_max = a.m;
@@ -42,13 +57,6 @@ __device__ __forceinline__ Stats row_stats(const VocabArgs& v, const Segments& s
 // ---------------------------------------------------------------- alternatives
 // A value and its column as one number that orders alternatives: larger
 // values first, the lower column first among equals. 0: no alternative (-inf).
-__device__ __forceinline__ uint32_t order_of(float x) {
-  const uint32_t b = __float_as_uint(x + 0.f);  // -0 counts as 0
-  return (b & 0x80000000u) ? ~b : b | 0x80000000u;
-}
-__device__ __forceinline__ float order_value(uint32_t o) {
-  return __uint_as_float((o & 0x80000000u) ? o & 0x7FFFFFFFu : ~o);
-}
 __device__ __forceinline__ uint64_t key_of(float x, uint32_t column) {
   if (!(x > -INFINITY)) return 0;
   return static_cast<uint64_t>(order_of(x)) << 32 | (0xFFFFFFFFu - column);
@@ -60,43 +68,55 @@ __device__ __forceinline__ int64_t key_column(uint64_t k) {
   return static_cast<int64_t>(0xFFFFFFFFu - static_cast<uint32_t>(k));
 }
 
-// One warp: a value that at least k of the threads' maxima (as orders) reach,
-// and not many more. Bisection: a comparison of all pairs of maxima instead
-// took 1300 instructions a warp, and most of a decode batch's time.
-__device__ __forceinline__ float warp_threshold(const uint32_t* order, int k) {
-  constexpr int N = kThreads / 32;
-  uint32_t mine[N], least = 0xFFFFFFFFu, most = 0;
+// One warp: a coarse order that at least k of the n maxima reach, and not many
+// more; 0 if there are fewer than k. Bisection: a comparison of all pairs of
+// maxima instead took 1300 instructions a warp, and most of a decode batch's
+// time. The first 256 maxima are kept in registers.
+__device__ __forceinline__ uint32_t warp_threshold(const uint16_t* maxima, int n, int k) {
+  constexpr int N = kWarps;
+  const int lane = threadIdx.x & 31;
+  if (n < k) return 0;
+  uint32_t mine[N], least = 0xFFFFu, most = 0;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    mine[i] = order[i * 32 + (threadIdx.x & 31)];
-    least = min(least, mine[i]);
+    const int at = i * 32 + lane;
+    mine[i] = at < n ? maxima[at] : 0;  // 0: below every order, and below every middle
     most = max(most, mine[i]);
+    if (at < n) least = min(least, mine[i]);
+  }
+  for (int i = N * 32 + lane; i < n; i += 32) {
+    least = min(least, static_cast<uint32_t>(maxima[i]));
+    most = max(most, static_cast<uint32_t>(maxima[i]));
   }
   uint32_t lo = __reduce_min_sync(0xFFFFFFFFu, least), hi = __reduce_max_sync(0xFFFFFFFFu, most);
-  // lo is reached by at least k; nothing above hi is reached at all
+  // lo is reached by all; nothing is above hi
   while (lo < hi) {
     const uint32_t mid = lo + (hi - lo + 1) / 2;
-    int n = 0;
+    int c = 0;
 #pragma unroll
-    for (int i = 0; i < N; ++i) n += mine[i] >= mid;
-    n = __reduce_add_sync(0xFFFFFFFFu, n);
-    if (n < k) {
+    for (int i = 0; i < N; ++i) c += mine[i] >= mid;
+#pragma unroll 8
+    for (int i = N * 32 + lane; i < n; i += 32) c += maxima[i] >= mid;
+    c = __reduce_add_sync(0xFFFFFFFFu, c);
+    if (c < k) {
       hi = mid - 1;
       continue;
     }
     lo = mid;
-    if (n <= k + k / 8) break;
+    if (c <= k + k / 8) break;
   }
-  return order_value(lo);
+  return lo;
 }
 
 struct TopSlots {
   uint64_t candidate[kMaxCandidates];
   uint64_t sorted[kMaxTop];
-  uint32_t order[kThreads];  // every thread's maximum
-  uint32_t work[kMaxWork];   // entry * kThreads + thread
-  int candidates, works;
-  float threshold;
+  uint32_t work[kMaxWork];  // entry * threads + thread
+  uint16_t order[kWarps * 32];  // every thread's maximum
+  int count[kWarps];
+  uint64_t kept[kMaxTop + 32];
+  int candidates, works, keeps;
+  uint32_t threshold;
   int found;
 };
 
@@ -107,13 +127,54 @@ __device__ __forceinline__ void offer(TopSlots& t, float x, uint32_t column) {
   if (i < kMaxCandidates) t.candidate[i] = k;
 }
 
+constexpr int kSpare = 32;  // candidates beyond the k best that are sorted rather than told apart
+// The candidates that are among the best k, and at most kSpare more, into
+// t.kept; returns how many. n > k. All threads.
+__device__ __noinline__ int keep_best(TopSlots& t, int n, int k) {
+  const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint64_t lo = 0, hi = ~0ull;  // all n reach lo, none is above hi; keys differ
+  int kept = n;
+  while (kept > k + kSpare) {
+    const uint64_t mid = lo + (hi - lo) / 2 + 1;
+    int c = 0;
+    for (int i = threadIdx.x; i < n; i += blockDim.x) c += t.candidate[i] >= mid;
+    c = __reduce_add_sync(0xFFFFFFFFu, c);
+    if (warps > 1) {
+      __syncthreads();
+      if (lane == 0) t.count[warp] = c;
+      __syncthreads();
+      c = 0;
+      for (int w = 0; w < warps; ++w) c += t.count[w];
+    }
+    if (c < k) {
+      hi = mid - 1;
+    } else {
+      lo = mid;
+      kept = c;
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) t.keeps = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += blockDim.x)
+    if (t.candidate[i] >= lo) t.kept[atomicAdd(&t.keeps, 1)] = t.candidate[i];
+  __syncthreads();
+  return kept;
+}
+
 // The best k of the first n candidates, sorted, into t.sorted; t.found of
 // them. Keys differ, so a key's place is the number of larger ones. All threads.
 __device__ void sort_candidates(TopSlots& t, int n, int k) {
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const uint64_t mine = t.candidate[i];
+  const uint64_t* keys = t.candidate;
+  if (n > k + kSpare) {
+    n = keep_best(t, n, k);
+    keys = t.kept;
+  }
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const uint64_t mine = keys[i];
     int place = 0;
-    for (int j = 0; j < n; ++j) place += t.candidate[j] > mine;
+#pragma unroll 8
+    for (int j = 0; j < n; ++j) place += keys[j] > mine;
     if (place < k) t.sorted[place] = mine;
   }
   if (threadIdx.x == 0) t.found = min(n, k);
@@ -132,14 +193,14 @@ __device__ __noinline__ void select_by_scan(const VocabArgs& v, const Segments& 
   const auto prune = [&](bool last) {
     __syncthreads();
     const int n = t.candidates;
-    if (!last && n <= kMaxCandidates - kThreads) {
+    if (!last && n <= kMaxCandidates - static_cast<int>(blockDim.x)) {
       __syncthreads();  // nobody adds before everybody has read
       return;
     }
     sort_candidates(t, n, k);
     if (!last) {
       if (t.found == k) floor_key = t.sorted[k - 1];
-      for (int i = threadIdx.x; i < t.found; i += kThreads) t.candidate[i] = t.sorted[i];
+      for (int i = threadIdx.x; i < t.found; i += blockDim.x) t.candidate[i] = t.sorted[i];
       if (threadIdx.x == 0) t.candidates = t.found;
       __syncthreads();
     }
@@ -150,7 +211,7 @@ __device__ __noinline__ void select_by_scan(const VocabArgs& v, const Segments& 
   };
   __syncthreads();
   ChunkWalk w(v.cut, lo + threadIdx.x / 32);
-  for (uint32_t i = lo; i < hi; i += kThreads / 32, w.next(v.cut, v.step)) {
+  for (uint32_t i = lo; i < hi; i += blockDim.x / 32, w.next(v.cut, v.step)) {
     for (int k = 0; k < kBatch; ++k) {
       const bool on = w.index < hi && w.vector() + k * 32 < w.vectors(v);
       const uint32_t col = on ? seg.head[w.seg] + (w.vector() + k * 32) * K : 0;
@@ -158,7 +219,7 @@ __device__ __noinline__ void select_by_scan(const VocabArgs& v, const Segments& 
         take(on, on ? load_one<DT>(seg.at<DT>(w.seg, col + j)) : 0.f, w.seg * v.shard + col + j);
     }
   }
-  for (uint32_t e0 = 0; edges && e0 < v.cut.edges; e0 += kThreads) {
+  for (uint32_t e0 = 0; edges && e0 < v.cut.edges; e0 += blockDim.x) {
     const uint32_t e = e0 + threadIdx.x;
     const bool on = e < v.cut.edges;
     uint32_t es = 0, col = 0;
@@ -168,39 +229,47 @@ __device__ __noinline__ void select_by_scan(const VocabArgs& v, const Segments& 
   prune(true);
 }
 
+// the stored maxima of a thread of warp 0, with four a chunk
+__device__ __forceinline__ int set_maxima(uint32_t chunks, int warps) {
+  return (chunks + warps - 1) / warps * kBatch;
+}
+
 // The best k columns among this CTA's chunks [lo, hi) and edge elements,
-// sorted, in t.sorted[0 .. t.found). A value that k of the threads' maxima
-// reach is at most the k-th largest element, so only the lanes' shares of
-// chunks whose maximum reaches it are read again.
+// sorted, in t.sorted[0 .. t.found). A value that k maxima of disjoint parts of
+// the row reach is at most the k-th largest element, so only the stored maxima
+// that reach it have their vectors read again.
 template <int DT>
 __device__ void select_top(const VocabArgs& v, const Segments& seg, uint32_t lo, uint32_t hi, bool edges,
-                           TopSlots& t, int k, const uint16_t* tops, int shift,
-                           float thread_max, bool slow) {
+                           TopSlots& t, int k, const uint16_t* tops, int shift, float thread_max, bool slow) {
   constexpr int K = Elem<DT>::kVec;
   if (slow) {  // the maxima were clamped
     select_by_scan<DT>(v, seg, lo, hi, edges, t, k);
     return;
   }
-  t.order[threadIdx.x] = order_of(thread_max);
+  const int threads = blockDim.x, warps = threads / 32, warp = threadIdx.x / 32;
+  const int chunks = lo + warp < hi ? (hi - lo - warp + warps - 1) / warps : 0;
+  const int entries = shift < 0 ? chunks * kBatch : (chunks + (1 << shift) - 1) >> shift;
+  t.order[threadIdx.x] = coarse_order(thread_max);
   if (threadIdx.x == 0) t.candidates = t.works = 0;
   __syncthreads();
   if (threadIdx.x < 32) {
-    const float found = warp_threshold(t.order, k);
+    // the threads' maxima or, where too few threads have one, the vectors': warp
+    // 0 has as many chunks as any, so the entries up to its last are set or empty
+    const uint32_t found = shift < 0 ? warp_threshold(tops, set_maxima(hi - lo, warps) * threads, k)
+                                     : warp_threshold(t.order, threads, k);
     if (threadIdx.x == 0) t.threshold = found;
   }
   __syncthreads();
-  const float threshold = t.threshold;
-  const auto reaches = [&](float x) { return x >= threshold && x > kClamp; };
-  const int warps = kThreads / 32, warp = threadIdx.x / 32;
-  const int chunks = lo + warp < hi ? (hi - lo - warp + warps - 1) / warps : 0;
-  const int entries = (chunks + (1 << shift) - 1) >> shift;
+  const uint32_t threshold = max(t.threshold, coarse_order(kClamp) + 1);  // and above the clamp
+  const auto reaches = [&](float x) { return coarse_order(x) >= threshold; };
+#pragma unroll 8
   for (int i = 0; i < entries; ++i) {
-    if (reaches(__uint_as_float(static_cast<uint32_t>(tops[i * kThreads + threadIdx.x]) << 16))) {
+    if (tops[i * threads + threadIdx.x] >= threshold) {
       const int n = atomicAdd(&t.works, 1);
-      if (n < kMaxWork) t.work[n] = i * kThreads + threadIdx.x;
+      if (n < kMaxWork) t.work[n] = i * threads + threadIdx.x;
     }
   }
-  for (uint32_t e = threadIdx.x; edges && e < v.cut.edges; e += kThreads) {
+  for (uint32_t e = first_edge(v, edges); e < v.cut.edges; e += next_edge(v)) {
     uint32_t es, col;
     edge_at<DT>(v, seg, e, es, col);
     const float x = load_one<DT>(seg.at<DT>(es, col));
@@ -208,20 +277,35 @@ __device__ void select_top(const VocabArgs& v, const Segments& seg, uint32_t lo,
   }
   __syncthreads();
   if (t.works <= kMaxWork) {
-    const int per = kBatch << shift, items = t.works * per;
-    for (int i = threadIdx.x; i < items; i += kThreads) {
-      const uint32_t job = t.work[i / per], thread = job % kThreads;
-      const uint32_t chunk = lo + ((job / kThreads << shift) + i % per / kBatch) * warps + thread / 32;
-      if (chunk >= hi) continue;
-      const ChunkWalk w(v.cut, chunk);
-      const uint32_t vec = w.part * kChunkVectors + i % kBatch * 32 + thread % 32;
-      if (vec >= w.vectors(v)) continue;
-      const uint32_t col = seg.head[w.seg] + vec * K;
-      Vec<DT> x;
-      x.set(dev::ld_global_v4(seg.at<DT>(w.seg, col)));
+    const int per = shift < 0 ? 1 : kBatch << shift, items = t.works * per;
+    // two vectors a thread at a time: their loads are what this waits for
+    for (int i0 = threadIdx.x; i0 < items; i0 += 2 * threads) {
+      Vec<DT> x[2];
+      uint32_t column[2];
 #pragma unroll
-      for (int j = 0; j < K; ++j)
-        if (reaches(x.get(j))) offer(t, x.get(j), w.seg * v.shard + col + j);
+      for (int h = 0; h < 2; ++h) {
+        const int i = i0 + h * threads;
+        column[h] = 0xFFFFFFFFu;
+        if (i >= items) continue;
+        const uint32_t job = t.work[i / per], thread = job % threads, entry = job / threads;
+        // the lane's chunk of this thread's, and the vector in it
+        const uint32_t nth = shift < 0 ? entry / kBatch : (entry << shift) + i % per / kBatch;
+        const uint32_t which = shift < 0 ? entry % kBatch : i % kBatch, chunk = lo + nth * warps + thread / 32;
+        if (chunk >= hi) continue;
+        const ChunkWalk w(v.cut, chunk);
+        const uint32_t vec = w.part * kChunkVectors + which * 32 + thread % 32;
+        if (vec >= w.vectors(v)) continue;
+        const uint32_t col = seg.head[w.seg] + vec * K;
+        column[h] = w.seg * v.shard + col;
+        x[h].set(dev::ld_global_v4(seg.at<DT>(w.seg, col)));
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (column[h] == 0xFFFFFFFFu) continue;
+#pragma unroll
+        for (int j = 0; j < K; ++j)
+          if (reaches(x[h].get(j))) offer(t, x[h].get(j), column[h] + j);
+      }
     }
   }
   __syncthreads();
@@ -243,8 +327,8 @@ struct ClusterTop {
   int place[kMaxTop];
 };
 
-template <int DT, bool TOP>
-__global__ void __launch_bounds__(kThreads, 5) log_probs_kernel(const __grid_constant__ LogProbsArgs a) {
+template <int DT, bool TOP, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, WARPS == kWarps ? (TOP ? 4 : 5) : 16 / WARPS) log_probs_kernel(const __grid_constant__ LogProbsArgs a) {
   extern __shared__ __align__(16) unsigned char dynamic[];
   __shared__ Segments seg;
   __shared__ JoinSlots slots;
@@ -264,7 +348,10 @@ __global__ void __launch_bounds__(kThreads, 5) log_probs_kernel(const __grid_con
     Stats st{0.f, 0.f, 0.f};
     float x = 0.f, thread_max = 0.f;
     if (scored) {
-      __syncthreads();  // the last row's segments are done with
+      __syncthreads();  // the last row's segments and maxima are done with
+      // a warp without a chunk stores no maxima
+      if (TOP && a.entry_shift < 0)
+        for (int i = 0; i < a.entries; ++i) tops[i * blockDim.x + threadIdx.x] = 0;
       set_segments<DT>(v, t, seg);
       __syncthreads();
       if (a.tokens && threadIdx.x == 0)
@@ -290,19 +377,19 @@ __global__ void __launch_bounds__(kThreads, 5) log_probs_kernel(const __grid_con
       const int mine = top->found;
       if (ctas == 1) {
         found = mine;
-        for (int i = threadIdx.x; i < mine; i += kThreads) {
+        for (int i = threadIdx.x; i < mine; i += blockDim.x) {
           out_lp[i] = st.log_prob(key_value(top->sorted[i]), v.inv_temp);
           out_id[i] = key_column(top->sorted[i]);
         }
       } else {
         // every CTA gets every CTA's sorted list and places its own keys by
         // the number of larger ones in each list
-        for (int i = threadIdx.x; i < mine * static_cast<int>(ctas); i += kThreads)
+        for (int i = threadIdx.x; i < mine * static_cast<int>(ctas); i += blockDim.x)
           remote_store(remote(&both->list[cta][i / ctas], i % ctas), top->sorted[i / ctas]);
         if (threadIdx.x < ctas) remote_store(remote(&both->count[cta], threadIdx.x), static_cast<uint64_t>(mine));
         if (threadIdx.x < k) both->place[threadIdx.x] = 0;
         cluster_barrier();
-        for (int i = threadIdx.x; i < mine * static_cast<int>(ctas); i += kThreads) {
+        for (int i = threadIdx.x; i < mine * static_cast<int>(ctas); i += blockDim.x) {
           const uint64_t key = top->sorted[i / ctas];
           const uint64_t* list = both->list[i % ctas];
           int l = 0, h = static_cast<int>(both->count[i % ctas]);
@@ -314,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 5) log_probs_kernel(const __grid_con
           if (l) atomicAdd(&both->place[i / ctas], l);
         }
         __syncthreads();
-        for (int i = threadIdx.x; i < mine; i += kThreads) {
+        for (int i = threadIdx.x; i < mine; i += blockDim.x) {
           const int place = both->place[i];
           if (place >= k) continue;
           out_lp[place] = st.log_prob(key_value(top->sorted[i]), v.inv_temp);
@@ -324,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 5) log_probs_kernel(const __grid_con
       }
     }
     if (cta == 0)
-      for (int i = found + threadIdx.x; i < k; i += kThreads) {
+      for (int i = found + threadIdx.x; i < k; i += blockDim.x) {
         out_lp[i] = scored && st.bad() ? NAN : -INFINITY;
         out_id[i] = -1;
       }
@@ -333,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 5) log_probs_kernel(const __grid_con
 
 // ---------------------------------------------------------------- distillation
 template <int DT>
-__global__ void __launch_bounds__(kThreads, 5) distill_kernel(const __grid_constant__ DistillArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, 5) distill_kernel(const __grid_constant__ DistillArgs a) {
   __shared__ Segments seg;
   __shared__ JoinSlots slots;
   __shared__ Entries entries;
@@ -366,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 5) distill_kernel(const __grid_const
 int cluster_for(const VocabArgs& v, const VocabLaunch& l) {
   int c = 1;
   while (c < kForwardCluster && v.rows * c * 2 <= static_cast<uint64_t>(l.sm_count) * 4 &&
-         v.cut.chunks >= static_cast<uint32_t>(2 * c * kThreads / 32) && (l.cap <= 0 || 2 * c <= l.cap))
+         v.cut.chunks >= static_cast<uint32_t>(2 * c * kWarps) && (l.cap <= 0 || 2 * c <= l.cap))
     c *= 2;
   return c;
 }
@@ -379,29 +466,50 @@ uint64_t grid_for(const VocabArgs& v, const VocabLaunch& l, int cluster) {
   return (rows < most ? rows : most) * cluster;
 }
 
+// Warps of a CTA: fewer for short rows, where there are rows enough for all SMs.
+int warps_for(const VocabArgs& v, const VocabLaunch& l) {
+  if (v.rows < static_cast<uint64_t>(l.sm_count) * 4) return kWarps;
+  return v.cut.chunks <= 2 ? 1 : v.cut.chunks <= 8 ? 2 : kWarps;
+}
+
+template <int DT, bool TOP, int WARPS>
+int launch_log_probs_w(LogProbsArgs& a, VocabLaunch& l) {
+  const int c = WARPS == kWarps ? cluster_for(a.v, l) : 1;
+  size_t smem = 0;
+  a.entry_shift = a.entries = 0;
+  if (TOP) {
+    const uint32_t per = (a.v.cut.chunks + c - 1) / c, most = (per + WARPS - 1) / WARPS;
+    const uint32_t lanes = (per < WARPS ? per : WARPS) * 32;  // that have a chunk
+    if (lanes < static_cast<uint32_t>(4 * a.top_k) && most * kBatch <= kMaxEntries) {
+      a.entry_shift = -2;  // too few to tell a threshold from
+      a.entries = static_cast<int>(most * kBatch);
+    } else {
+      while (((most + (1u << a.entry_shift) - 1) >> a.entry_shift) > kMaxEntries) ++a.entry_shift;
+      a.entries = static_cast<int>((most + (1u << a.entry_shift) - 1) >> a.entry_shift);
+    }
+    smem = sizeof(TopSlots) + (c > 1 ? sizeof(ClusterTop) : 0) + sizeof(uint16_t) * WARPS * 32 * a.entries;
+    const cudaError_t e = cudaFuncSetAttribute(log_probs_kernel<DT, TOP, WARPS>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return static_cast<int>(e);
+  }
+  return launch_rows(log_probs_kernel<DT, TOP, WARPS>, a, l, grid_for(a.v, l, c), WARPS * 32, c, smem);
+}
+
 template <int DT, bool TOP>
 int launch_log_probs_t(LogProbsArgs& a, VocabLaunch& l) {
   set_cut<DT>(a.v, 0);
-  const int c = cluster_for(a.v, l);
-  size_t smem = 0;
-  a.entry_shift = 0;
-  if (TOP) {
-    const uint32_t per = (a.v.cut.chunks + c - 1) / c, warps = kThreads / 32, most = (per + warps - 1) / warps;
-    while (((most + (1u << a.entry_shift) - 1) >> a.entry_shift) > kMaxEntries) ++a.entry_shift;
-    const uint32_t entries = (most + (1u << a.entry_shift) - 1) >> a.entry_shift;
-    smem = sizeof(TopSlots) + (c > 1 ? sizeof(ClusterTop) : 0) + sizeof(uint16_t) * kThreads * entries;
-    const cudaError_t e = cudaFuncSetAttribute(log_probs_kernel<DT, TOP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(smem));
-    if (e != cudaSuccess) return static_cast<int>(e);
+  switch (warps_for(a.v, l)) {
+    case 1: return launch_log_probs_w<DT, TOP, 1>(a, l);
+    case 2: return launch_log_probs_w<DT, TOP, 2>(a, l);
+    default: return launch_log_probs_w<DT, TOP, kWarps>(a, l);
   }
-  return launch_rows(log_probs_kernel<DT, TOP>, a, l, grid_for(a.v, l, c), kThreads, c, smem);
 }
 
 template <int DT>
 int launch_distill_t(DistillArgs& a, VocabLaunch& l) {
   set_cut<DT>(a.v, 0);
   const int c = cluster_for(a.v, l);
-  return launch_rows(distill_kernel<DT>, a, l, grid_for(a.v, l, c), kThreads, c, 0);
+  return launch_rows(distill_kernel<DT>, a, l, grid_for(a.v, l, c), kWarps * 32, c, 0);
 }
 
 }  // namespace

@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(kThreads, kStepCtasPerSm) distill_step_kernel(
         return has_column<DT>(v, t, column, lo, hi, cta == 0);
       });
     }
-    Part p = scan_row<DT, false, true>(v, seg, lo, hi, cta == 0, KeepLoad(), [](float) {});
+    Part p = scan_row<DT, false, true>(v, seg, lo, hi, cta == 0, KeepLoad(), [](float, const Vec<DT>(&)[kBatch]) {});
     p = row_join(p, c, slots, phase, ctas);
     const bool fast = fabsf(p.m) < -kClamp;
     const Stats st = fast ? stats_of(p, c) : slow_stats<DT>(v, seg, lo, hi, slots, phase, cta, ctas);

@@ -51,7 +51,8 @@ struct LogProbsArgs {
   float* top_log_probs;
   int64_t* top_ids;
   int top_k;
-  int entry_shift;  // 2^entry_shift chunks share one stored maximum
+  int entry_shift;  // 2^entry_shift chunks share one stored maximum; -2: a chunk's four vectors have one each
+  int entries;      // stored maxima of a thread, at the most
 };
 
 struct LogProbsGradArgs {

@@ -159,6 +159,11 @@ __device__ __forceinline__ float batch_max(const Vec<DT> (&x)[N]) {
     for (int i = 0; i < 4; ++i) m = max_f32(m, __uint_as_float(x[k].w[i]));
   return m;
 }
+template <int DT>
+__device__ __forceinline__ float vector_max(const Vec<DT>& x) {
+  const Vec<DT> one[1] = {x};
+  return batch_max<DT, 1>(one);
+}
 
 // ---------------------------------------------------------------- statistics
 // Part of a row's softmax: the maximum m, s = sum 2^(x c - r) and
@@ -293,13 +298,13 @@ struct Segments {
   }
 };
 
-// thread r < used sets rank r's segment of row t; the caller synchronises
+// sets the segments of row t; the caller synchronises
 template <int DT>
 __device__ __forceinline__ void set_segments(const VocabArgs& v, uint64_t t, Segments& s) {
-  if (threadIdx.x < v.used) {
-    const char* at = static_cast<const char*>(v.p.src[threadIdx.x]) + t * v.src_stride * Elem<DT>::kBytes;
-    s.src[threadIdx.x] = at;
-    s.head[threadIdx.x] = static_cast<uint32_t>(-reinterpret_cast<uintptr_t>(at) & 15) / Elem<DT>::kBytes;
+  for (uint32_t r = threadIdx.x; r < v.used; r += blockDim.x) {
+    const char* at = static_cast<const char*>(v.p.src[r]) + t * v.src_stride * Elem<DT>::kBytes;
+    s.src[r] = at;
+    s.head[r] = static_cast<uint32_t>(-reinterpret_cast<uintptr_t>(at) & 15) / Elem<DT>::kBytes;
   }
 }
 
@@ -523,7 +528,7 @@ __device__ __forceinline__ float add_chunk(Part& a, float& r, f32x2 (&s)[2], f32
 
 // This thread's part of chunks [lo, hi) of the row, and of its edge elements
 // where `edges` is set. `load_vector(address)` loads 16 bytes;
-// `top_of(chunk's maximum)` is called once a chunk.
+// `top_of(chunk's maximum, its vectors)` is called once a chunk.
 template <int DT, bool ENTROPY, bool ANY, typename Load, typename TopF>
 __device__ __forceinline__ Part scan_row(const VocabArgs& v, const Segments& seg, uint32_t lo, uint32_t hi, bool edges,
                                          Load load_vector, TopF top_of) {
@@ -534,7 +539,8 @@ __device__ __forceinline__ Part scan_row(const VocabArgs& v, const Segments& seg
   for (ChunkWalk w(v.cut, first_chunk(v, lo, hi)); w.index < hi; w.next(v.cut, v.step)) {
     Vec<DT> x[kBatch];
     load_chunk<DT, ANY>(v, seg.at<DT>(w.seg, seg.head[w.seg]), w, x, load_vector);
-    top_of(add_chunk<DT, ENTROPY>(a, r, s, u, x, c));
+    const float top = add_chunk<DT, ENTROPY>(a, r, s, u, x, c);
+    top_of(top, x);
   }
   float s0, s1, s2, s3;
   unpack(s[0], s0, s1);

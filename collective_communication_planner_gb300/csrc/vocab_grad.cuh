@@ -35,10 +35,10 @@ __device__ __forceinline__ void set_segment(const VocabArgs& v, uint64_t t, uint
   s.head[r] = head_of<DT>(v, dst);
 }
 
-// thread r < used sets rank r's segment of row t; the caller synchronises
+// sets the segments of row t; the caller synchronises
 template <int DT>
 __device__ __forceinline__ void set_segments(const VocabArgs& v, uint64_t t, GradSegments& s) {
-  if (threadIdx.x < v.used) set_segment<DT>(v, t, threadIdx.x, s);
+  for (uint32_t r = threadIdx.x; r < v.used; r += blockDim.x) set_segment<DT>(v, t, r, s);
 }
 
 // One row's gradient y = p (scale + slope log2 p); columns that a token or a
