@@ -327,8 +327,8 @@ struct ClusterTop {
   int place[kMaxTop];
 };
 
-template <int DT, bool TOP, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32, WARPS == kWarps ? (TOP ? 4 : 5) : 16 / WARPS) log_probs_kernel(const __grid_constant__ LogProbsArgs a) {
+template <int DT, bool TOP>
+__global__ void __launch_bounds__(kWarps * 32, TOP ? 4 : 5) log_probs_kernel(const __grid_constant__ LogProbsArgs a) {
   extern __shared__ __align__(16) unsigned char dynamic[];
   __shared__ Segments seg;
   __shared__ JoinSlots slots;
@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == kWarps ? (TOP ? 4 : 5) : 
 
 // ---------------------------------------------------------------- distillation
 template <int DT>
-__global__ void __launch_bounds__(kWarps * 32, 5) distill_kernel(const __grid_constant__ DistillArgs a) {
+__global__ void __launch_bounds__((kWarps + 1) * 32, 4) distill_kernel(const __grid_constant__ DistillArgs a) {
   __shared__ Segments seg;
   __shared__ JoinSlots slots;
   __shared__ Entries entries;
@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(kWarps * 32, 5) distill_kernel(const __grid_co
     __syncthreads();  // the last row's segments are done with
     set_segments<DT>(v, t, seg);
     __syncthreads();
-    const bool mine = cta == 0 && threadIdx.x < 32;
+    const bool mine = cta == 0 && threadIdx.x >= v.step.warps * 32;  // the warp behind those that stream
     if (mine) {
       const TeacherRow q = read_teacher(a, t);
       uint32_t x[kMaxTop / 32];
@@ -466,20 +466,31 @@ uint64_t grid_for(const VocabArgs& v, const VocabLaunch& l, int cluster) {
   return (rows < most ? rows : most) * cluster;
 }
 
-// Warps of a CTA: fewer for short rows, where there are rows enough for all SMs.
-int warps_for(const VocabArgs& v, const VocabLaunch& l) {
-  if (v.rows < static_cast<uint64_t>(l.sm_count) * 4) return kWarps;
-  return v.cut.chunks <= 2 ? 1 : v.cut.chunks <= 8 ? 2 : kWarps;
+// Warps of a CTA that stream a row. Few rows take eight (and clusters of CTAs).
+// Many short ones take fewer, so that more rows are in flight: what a row costs
+// beside its bytes is latency. GB300, 4096 rows bf16, 1 / 4 / 8 warps: 1000
+// columns 6 / 11 / 18 us, with 5 alternatives 15 / 28 / 48; 8192 columns 17 /
+// 19 / 24, with 5 alternatives 28 / 34 / 52, with 64 66 / 58 / 67. Long rows
+// take eight when they are many (131072 columns, 4096 rows: 164 us with four,
+// 158), or when a threshold for many alternatives needs the maxima of all those
+// threads (1024 rows, 64 alternatives: 71, 64); else four (777 x 50021 fp32: 29, 34).
+int warps_for(const VocabArgs& v, const VocabLaunch& l, int top_k) {
+  const uint64_t sms = l.sm_count;
+  if (v.rows < sms * 4) return kWarps;
+  if (v.cut.chunks <= (top_k ? 1u : 4u)) return 1;
+  return v.cut.chunks <= 64 || (v.rows < sms * 12 && top_k <= 16) ? 4 : kWarps;
 }
 
-template <int DT, bool TOP, int WARPS>
-int launch_log_probs_w(LogProbsArgs& a, VocabLaunch& l) {
-  const int c = WARPS == kWarps ? cluster_for(a.v, l) : 1;
+template <int DT, bool TOP>
+int launch_log_probs_t(LogProbsArgs& a, VocabLaunch& l) {
+  set_cut<DT>(a.v, 0);
+  const uint32_t warps = warps_for(a.v, l, a.top_k);
+  const int c = cluster_for(a.v, l);
   size_t smem = 0;
   a.entry_shift = a.entries = 0;
   if (TOP) {
-    const uint32_t per = (a.v.cut.chunks + c - 1) / c, most = (per + WARPS - 1) / WARPS;
-    const uint32_t lanes = (per < WARPS ? per : WARPS) * 32;  // that have a chunk
+    const uint32_t per = (a.v.cut.chunks + c - 1) / c, most = (per + warps - 1) / warps;
+    const uint32_t lanes = (per < warps ? per : warps) * 32;  // that have a chunk
     if (lanes < static_cast<uint32_t>(4 * a.top_k) && most * kBatch <= kMaxEntries) {
       a.entry_shift = -2;  // too few to tell a threshold from
       a.entries = static_cast<int>(most * kBatch);
@@ -487,29 +498,19 @@ int launch_log_probs_w(LogProbsArgs& a, VocabLaunch& l) {
       while (((most + (1u << a.entry_shift) - 1) >> a.entry_shift) > kMaxEntries) ++a.entry_shift;
       a.entries = static_cast<int>((most + (1u << a.entry_shift) - 1) >> a.entry_shift);
     }
-    smem = sizeof(TopSlots) + (c > 1 ? sizeof(ClusterTop) : 0) + sizeof(uint16_t) * WARPS * 32 * a.entries;
-    const cudaError_t e = cudaFuncSetAttribute(log_probs_kernel<DT, TOP, WARPS>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    smem = sizeof(TopSlots) + (c > 1 ? sizeof(ClusterTop) : 0) + sizeof(uint16_t) * warps * 32 * a.entries;
+    const cudaError_t e = cudaFuncSetAttribute(log_probs_kernel<DT, TOP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(smem));
     if (e != cudaSuccess) return static_cast<int>(e);
   }
-  return launch_rows(log_probs_kernel<DT, TOP, WARPS>, a, l, grid_for(a.v, l, c), WARPS * 32, c, smem);
-}
-
-template <int DT, bool TOP>
-int launch_log_probs_t(LogProbsArgs& a, VocabLaunch& l) {
-  set_cut<DT>(a.v, 0);
-  switch (warps_for(a.v, l)) {
-    case 1: return launch_log_probs_w<DT, TOP, 1>(a, l);
-    case 2: return launch_log_probs_w<DT, TOP, 2>(a, l);
-    default: return launch_log_probs_w<DT, TOP, kWarps>(a, l);
-  }
+  return launch_rows(log_probs_kernel<DT, TOP>, a, l, grid_for(a.v, l, c), warps * 32, c, smem);
 }
 
 template <int DT>
 int launch_distill_t(DistillArgs& a, VocabLaunch& l) {
   set_cut<DT>(a.v, 0);
-  const int c = cluster_for(a.v, l);
-  return launch_rows(distill_kernel<DT>, a, l, grid_for(a.v, l, c), kWarps * 32, c, 0);
+  const int c = cluster_for(a.v, l), warps = warps_for(a.v, l, 0);
+  return launch_rows(distill_kernel<DT>, a, l, grid_for(a.v, l, c), (warps + 1) * 32, c, 0, warps);
 }
 
 }  // namespace

@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kThreads, 5) distill_grad_kernel(const __grid_
     store_edges<DT>(v, seg, g, t, it.part, v.parts);
     if (!zero) {
       __syncthreads();
-      if (threadIdx.x < named.count) store_named<DT>(v, t, named, g, w, threadIdx.x);
+      for (int i = threadIdx.x; i < named.count; i += blockDim.x) store_named<DT>(v, t, named, g, w, i);
     }
   }
 }
@@ -94,17 +94,19 @@ template <int DT, typename Args>
 int launch_parts(void (*kernel)(Args), Args& a, VocabLaunch& l) {
   VocabArgs& v = a.v;
   set_cut<DT>(v, v.together ? 0 : 2);
+  const auto parts = [](uint32_t chunks, uint32_t share) { return chunks > share ? (chunks + share - 1) / share : 1; };
+  // a short row: a CTA of as many warps as it has chunks
+  uint32_t warps = kThreads / 32;
+  while (warps > 1 && v.cut.chunks <= warps / 2) warps /= 2;
   // an item is at most eight chunks a warp; fewer where that leaves SMs
   // without four items
-  constexpr uint32_t kWarps = kThreads / 32;
   uint32_t deep = 8;
-  while (deep > 1 && v.rows * ((v.cut.chunks + deep * kWarps - 1) / (deep * kWarps)) < static_cast<uint64_t>(l.sm_count) * 4)
-    deep /= 2;
-  v.parts = v.cut.chunks > deep * kWarps ? (v.cut.chunks + deep * kWarps - 1) / (deep * kWarps) : 1;
+  while (deep > 1 && v.rows * parts(v.cut.chunks, deep * warps) < static_cast<uint64_t>(l.sm_count) * 4) deep /= 2;
+  v.parts = parts(v.cut.chunks, deep * warps);
   uint64_t grid = v.rows * v.parts;
   const uint64_t most = l.cap > 0 ? static_cast<uint64_t>(l.cap) : static_cast<uint64_t>(1) << 30;
   if (grid > most) grid = most;
-  return launch_rows(kernel, a, l, grid, kThreads, 1, 0);
+  return launch_rows(kernel, a, l, grid, warps * 32, 1, 0);
 }
 
 }  // namespace

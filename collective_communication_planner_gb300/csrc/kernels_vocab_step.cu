@@ -6,7 +6,7 @@ namespace {
 
 using namespace vocab;
 
-constexpr int kWarps = 8;                    // that stream; one more reads the teacher's entries
+constexpr int kWarps = 8;  // that stream, at the most; one more reads the teacher's entries
 constexpr int kThreads = (kWarps + 1) * 32;
 constexpr uint64_t kKeepBytes = 52ull << 20;  // rows that L2 keeps between two reads
 constexpr int kStepCluster = 8;
@@ -33,7 +33,7 @@ __global__ void __launch_bounds__(kThreads, kStepCtasPerSm) distill_step_kernel(
     set_segments<DT>(v, t, seg);
     __syncthreads();
     const float w = a.weights[t] * v.inv_temp;
-    if (threadIdx.x >= kWarps * 32) {
+    if (threadIdx.x >= v.step.warps * 32) {
       const TeacherRow q = read_teacher(a, t);
       uint32_t x[kMaxTop / 32];
       load_named<DT>(v, t, q, x);
@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(kThreads, kStepCtasPerSm) distill_step_kernel(
     p = row_join(p, c, slots, phase, ctas);
     const bool fast = fabsf(p.m) < -kClamp;
     const Stats st = fast ? stats_of(p, c) : slow_stats<DT>(v, seg, lo, hi, slots, phase, cta, ctas);
-    if (cta == 0 && threadIdx.x >= kWarps * 32) store_loss(a, t, named, st);
+    if (cta == 0 && threadIdx.x >= v.step.warps * 32) store_loss(a, t, named, st);
     RowGrad g;
     g.set(v, st.max, st.log2_s, w * named.total, 0.f);
     g.zero = w == 0.f || named.total == 0.f || st.empty();
@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(kThreads, kStepCtasPerSm) distill_step_kernel(
     store_edges<DT>(v, seg, g, t, cta, ctas);
     if (!g.zero) {
       __syncthreads();
-      if (threadIdx.x < named.count) store_named<DT>(v, t, named, g, w, threadIdx.x);
+      for (int i = threadIdx.x; i < named.count; i += blockDim.x) store_named<DT>(v, t, named, g, w, i);
     }
   }
 }
@@ -74,10 +74,15 @@ int launch_step_t(DistillArgs& a, VocabLaunch& l) {
   while (c < kStepCluster && v.cut.chunks >= static_cast<uint32_t>(2 * c * kWarps) &&
          (l.cap <= 0 || 2 * c <= l.cap) && (v.rows * 2 * c <= resident || kept(c) > kKeepBytes))
     c *= 2;
+  // many short rows: fewer warps, so that more rows are in flight
+  int warps = kWarps;
+  while (warps > 1 && v.rows >= static_cast<uint64_t>(l.sm_count) * 4 && v.cut.chunks <= static_cast<uint32_t>(warps) * 2)
+    warps /= 2;
   uint64_t rows = v.rows;
   if (l.cap > 0 && rows * c > static_cast<uint64_t>(l.cap)) rows = l.cap / c;
   const uint64_t most = static_cast<uint64_t>(1) << 27;
-  return launch_rows(distill_step_kernel<DT>, a, l, (rows < most ? rows : most) * c, kThreads, c, 0, kWarps);
+  return launch_rows(distill_step_kernel<DT>, a, l, (rows < most ? rows : most) * c, (warps + 1) * 32, c, 0,
+                     warps);
 }
 
 }  // namespace
