@@ -607,7 +607,7 @@ __device__ __forceinline__ TeacherEntries load_teacher(const DistillArgs& a, uin
 __device__ __forceinline__ TeacherRow teacher_row(const DistillArgs& a, const TeacherEntries& e) {
   constexpr int N = kMaxTop / 32;
   TeacherRow r;
-  float lse = e.lse, z[N];
+  float top = e.lse, rest = 0.f, z[N];  // the log-sum is top + rest
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const bool has = e.id[i] >= 0 && e.id[i] < a.v.vocab;
@@ -616,7 +616,8 @@ __device__ __forceinline__ TeacherRow teacher_row(const DistillArgs& a, const Te
     z[i] = has ? x * a.v.inv_temp : -INFINITY;
   }
   if (!a.teacher_lse) {
-    float top = -INFINITY, sum = 0.f;
+    float sum = 0.f;
+    top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < N; ++i) top = fmaxf(top, z[i]);
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
@@ -625,12 +626,12 @@ __device__ __forceinline__ TeacherRow teacher_row(const DistillArgs& a, const Te
     for (int i = 0; i < N; ++i)
       if (32 * i < a.top_k) sum += expf(z[i] - top);
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    lse = sum == 0.f ? 0.f : top + logf(sum);
+    rest = sum == 0.f ? 0.f : logf(sum);
   }
   r.total = 0.f;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    r.log_q[i] = z[i] - lse;
+    r.log_q[i] = (z[i] - top) - rest;
     r.q[i] = 32 * i < a.top_k ? expf(r.log_q[i]) : 0.f;
     r.total += r.q[i];
   }
