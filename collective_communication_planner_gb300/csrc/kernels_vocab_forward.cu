@@ -50,8 +50,7 @@ __device__ __forceinline__ Stats row_stats(const VocabArgs& v, const Segments& s
   });
   thread_max = a.m;
   a = row_join(a, v.exp2_scale, slots, phase, ctas);
-  if (fabsf(a.m) < -kClamp) return stats_of(a, v.exp2_scale);
-  return slow_stats<DT>(v, seg, lo, hi, slots, phase, cta, ctas);
+  return joined_stats<DT>(a, v, seg, lo, hi, slots, phase, cta, ctas);
 }
 
 // ---------------------------------------------------------------- alternatives
@@ -313,8 +312,31 @@ __device__ void select_top(const VocabArgs& v, const Segments& seg, uint32_t lo,
   bool whole = t.works > kMaxWork || n > kMaxCandidates;
   if (!whole && n < k) {
     // fewer than k columns above the clamp: there may be some below it
+    // (a warp reads four chunks at a time, past its last the last again: latency)
     bool below = false;
-    each_element<DT>(v, seg, lo, hi, edges, [&](float x) { below = below || (x <= kClamp && x > -INFINITY); });
+    for (uint32_t at = first_chunk(v, lo, hi); at < hi; at += 4 * v.step.warps) {
+      Vec<DT> x[4][kBatch];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const ChunkWalk w(v.cut, min(at + q * v.step.warps, hi - 1));
+        const char* body = seg.at<DT>(w.seg, seg.head[w.seg]);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+          x[q][i].set(dev::ld_global_v4(body + static_cast<uint64_t>(min(w.vector() + i * 32, w.vectors(v) - 1)) * 16));
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+          for (int j = 0; j < K; ++j) below |= x[q][i].get(j) <= kClamp && x[q][i].get(j) > -INFINITY;
+    }
+    for (uint32_t e = first_edge(v, edges); e < v.cut.edges; e += next_edge(v)) {
+      uint32_t es, col;
+      edge_at<DT>(v, seg, e, es, col);
+      const float x = load_one<DT>(seg.at<DT>(es, col));
+      below |= x <= kClamp && x > -INFINITY;
+    }
     whole = __syncthreads_or(below);
   }
   if (whole) select_by_scan<DT>(v, seg, lo, hi, edges, t, k);
@@ -448,11 +470,14 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 4) distill_kernel(const __g
   }
 }
 
-// CTAs of one row: as many as keep every SM at no more than four, but none
-// whose slice is less than one chunk of every warp.
+// CTAs of one row: as many as keep every SM at no more than two, but none whose
+// slice is less than one chunk of every warp. GB300, 131072 columns bf16 over
+// clusters of 1 / 2 / 4 / 8: one row 10.9 / 7.7 / 5.6 / 4.6 us, with 20
+// alternatives 15.3 / 12.4 / 10.1 / 10.2; 64 rows 11.1 / 8.0 / 6.8 / 8.3, with
+// 5 alternatives 16.6 / 14.0 / 13.3 / 15.1; 256 rows with 5: 23.7 / 27.3.
 int cluster_for(const VocabArgs& v, const VocabLaunch& l) {
   int c = 1;
-  while (c < kForwardCluster && v.rows * c * 2 <= static_cast<uint64_t>(l.sm_count) * 4 &&
+  while (c < kForwardCluster && v.rows * c * 2 <= static_cast<uint64_t>(l.sm_count) * 2 &&
          v.cut.chunks >= static_cast<uint32_t>(2 * c * kWarps) && (l.cap <= 0 || 2 * c <= l.cap))
     c *= 2;
   return c;
@@ -499,9 +524,11 @@ int launch_log_probs_t(LogProbsArgs& a, VocabLaunch& l) {
       a.entries = static_cast<int>((most + (1u << a.entry_shift) - 1) >> a.entry_shift);
     }
     smem = sizeof(TopSlots) + (c > 1 ? sizeof(ClusterTop) : 0) + sizeof(uint16_t) * warps * 32 * a.entries;
-    const cudaError_t e = cudaFuncSetAttribute(log_probs_kernel<DT, TOP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(smem));
-    if (e != cudaSuccess) return static_cast<int>(e);
+    if (smem > 48 * 1024) {  // more than a kernel gets unasked
+      const cudaError_t e = cudaFuncSetAttribute(log_probs_kernel<DT, TOP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 static_cast<int>(smem));
+      if (e != cudaSuccess) return static_cast<int>(e);
+    }
   }
   return launch_rows(log_probs_kernel<DT, TOP>, a, l, grid_for(a.v, l, c), warps * 32, c, smem);
 }

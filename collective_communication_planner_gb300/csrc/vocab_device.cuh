@@ -168,15 +168,18 @@ __device__ __forceinline__ float vector_max(const Vec<DT>& x) {
 // ---------------------------------------------------------------- statistics
 // Part of a row's softmax: the maximum m, s = sum 2^(x c - r) and
 // u = sum 2^(x c - r) (x c - r) with c = log2(e) / temperature and the
-// reference r = m c rounded to fp32. x c - r is one fused operation, so it is
-// exact but for one rounding however far the logits are from zero.
+// reference r = m c rounded to fp32, of the clamped m (m itself may be -inf).
+// x c - r is one fused operation, so it is exact but for one rounding however
+// far the logits are from zero.
 struct Part {
   float m, s, u;
 };
 
+__device__ __forceinline__ float reference(float m, float c) { return __fmul_rn(fmaxf(m, kClamp), c); }
+
 __device__ __forceinline__ void rebase(Part& a, float m, float c) {
   if (a.m == m) return;
-  const float d = __fsub_rn(__fmul_rn(a.m, c), __fmul_rn(m, c));
+  const float d = __fsub_rn(reference(a.m, c), reference(m, c));
   const float f = exp2_ftz(d);
   a.u = f == 0.f ? 0.f : f * (a.u + a.s * d);
   a.s *= f;
@@ -241,7 +244,7 @@ __device__ __forceinline__ Part row_join(Part a, float c, JoinSlots& slots, int&
   a = lanes_join<32>(a, c);
   if (lane == 0) slots.warp[phase][warp] = a;
   __syncthreads();
-  const Part none{kClamp, 0.f, 0.f};
+  const Part none{-INFINITY, 0.f, 0.f};
   a = lanes_join<32>(lane < warps ? slots.warp[phase][lane] : none, c);
   if (csize > 1) {
     if (warp == 0 && lane < csize) {
@@ -490,19 +493,28 @@ __device__ __noinline__ Stats slow_stats(const VocabArgs& v, const Segments& s, 
   return Stats{};
 }
 
+// The statistics of a row from its joined part.
+template <int DT>
+__device__ __forceinline__ Stats joined_stats(const Part& a, const VocabArgs& v, const Segments& s, uint32_t lo,
+                                              uint32_t hi, JoinSlots& slots, int& phase, uint32_t cta, uint32_t ctas) {
+  if (fabsf(a.m) < -kClamp) return stats_of(a, v.exp2_scale);
+  if (a.m == -INFINITY && a.s == a.s) return Stats{a.m, 0.f, 0.f};  // nothing but -inf, and no NaN
+  return slow_stats<DT>(v, s, lo, hi, slots, phase, cta, ctas);
+}
+
 // Adds a chunk's vectors to a thread's part: the largest element first, which
 // it returns, then the sums. s and u are relative to r = a.m c.
 template <int DT, bool ENTROPY>
 __device__ __forceinline__ float add_chunk(Part& a, float& r, f32x2 (&s)[2], f32x2 (&u)[2], Vec<DT> (&x)[kBatch],
                                            float c) {
+  const float top = batch_max<DT, kBatch>(x);
   // distances have to be finite for u only: 2^-inf is 0
   if (ENTROPY) {
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) x[k].clamp();
   }
-  const float top = batch_max<DT, kBatch>(x);
   if (top > a.m) {
-    const float to = __fmul_rn(top, c), d = __fsub_rn(r, to), f = exp2_ftz(d);
+    const float to = reference(top, c), d = __fsub_rn(r, to), f = exp2_ftz(d);
     const f32x2 dd = pack(d, d), ff = pack(f, f);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -533,8 +545,8 @@ template <int DT, bool ENTROPY, bool ANY, typename Load, typename TopF>
 __device__ __forceinline__ Part scan_row(const VocabArgs& v, const Segments& seg, uint32_t lo, uint32_t hi, bool edges,
                                          Load load_vector, TopF top_of) {
   const float c = v.exp2_scale;
-  Part a{kClamp, 0.f, 0.f};
-  float r = __fmul_rn(kClamp, c);
+  Part a{-INFINITY, 0.f, 0.f};
+  float r = reference(a.m, c);
   f32x2 s[2] = {0, 0}, u[2] = {0, 0};
   for (ChunkWalk w(v.cut, first_chunk(v, lo, hi)); w.index < hi; w.next(v.cut, v.step)) {
     Vec<DT> x[kBatch];
@@ -552,9 +564,9 @@ __device__ __forceinline__ Part scan_row(const VocabArgs& v, const Segments& seg
   for (uint32_t e = first_edge(v, edges); e < v.cut.edges; e += next_edge(v)) {
     uint32_t es, col;
     edge_at<DT>(v, seg, e, es, col);
-    const float x = max_f32(load_one<DT>(seg.at<DT>(es, col)), kClamp);
+    const float x = load_one<DT>(seg.at<DT>(es, col));
     if (x > a.m) rebase(a, x, c);
-    const float d = __fmaf_rn(x, c, -__fmul_rn(a.m, c)), p = exp2_ftz(d);
+    const float d = __fmaf_rn(max_f32(x, kClamp), c, -reference(a.m, c)), p = exp2_ftz(d);
     a.s += p;
     a.u = __fmaf_rn(p, d, a.u);
   }

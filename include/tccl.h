@@ -371,7 +371,7 @@ tcclResult_t tcclCopyOutInspect(int coll, int nranks, const void* const sendbufs
 
 /*
  * Test hook for the bounded-wait error path: while enabled, each bulk-engine
- * launch makes its first CTA wait on a barrier that nothing signals, with a
+ * launch (and each launch of tcclDistill's persistent kernel) makes its first CTA wait on a barrier that nothing signals, with a
  * `timeout_ms` bound; the CTA then records tcclDeviceTimeout, skips its
  * remaining work and exits normally (no trap, no fault). Other CTAs finish.
  */
@@ -552,6 +552,13 @@ tcclResult_t tcclLogProbsBackward(tcclGroup_t g, const void* const logits[],
  *   grads[.][t, j] = weights[t] (Q p_j - sum_{k: id_k = j} q_k) / temperature,
  * zeros where weights[t] is 0. stats may be null. Cross entropy with its
  * gradient is top_k = 1: the label, with any finite teacher logit.
+ *
+ * With a gradient, rows that are long and many run on a persistent kernel that
+ * keeps a row in the shared memory of a cluster between its sum and its
+ * gradient. Its waits are bounded by wait_timeout_ms: one that runs out is
+ * reported by tcclGroupQueryError as tcclDeviceTimeout, and the call's outputs
+ * are undefined then. The first such call asks the device how many clusters it
+ * holds; later ones of the group do not.
  */
 tcclResult_t tcclDistill(tcclGroup_t g, const void* const logits[], const tcclVocab_t* shape,
                          const int64_t* teacher_ids, const void* teacher_logits,
