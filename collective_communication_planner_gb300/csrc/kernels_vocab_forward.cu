@@ -49,7 +49,7 @@ __device__ __forceinline__ Stats row_stats(const VocabArgs& v, const Segments& s
     if ((++chunk & ((1 << shift) - 1)) == 0) entry = kClamp;
   });
   thread_max = a.m;
-  a = row_join(a, v.exp2_scale, slots, phase, ctas);
+  a = row_join(a, v.exp2_scale, slots, phase, v.step.warps, ctas);
   return joined_stats<DT>(a, v, seg, lo, hi, slots, phase, cta, ctas);
 }
 
@@ -366,29 +366,33 @@ __global__ void __launch_bounds__(kWarps * 32, TOP ? 4 : 5) log_probs_kernel(con
   int phase = 0;
   for (uint64_t t = blockIdx.x / ctas; t < v.rows; t += gridDim.x / ctas) {
     const int64_t token = a.tokens ? a.tokens[t] : 0;
-    const bool scored = token >= 0 && token < v.vocab;  // the same in every thread of the cluster
     Stats st{0.f, 0.f, 0.f};
     float x = 0.f, thread_max = 0.f;
+    __syncthreads();  // the last row's segments and maxima are done with
+    // a warp without a chunk stores no maxima
+    if (TOP && a.entry_shift < 0)
+      for (int i = 0; i < a.entries; ++i) tops[i * blockDim.x + threadIdx.x] = 0;
+    set_segments<DT>(v, t, seg);
+    __syncthreads();
+    const bool scored = token >= 0 && token < v.vocab;  // the same in every thread of the cluster
     if (scored) {
-      __syncthreads();  // the last row's segments and maxima are done with
-      // a warp without a chunk stores no maxima
-      if (TOP && a.entry_shift < 0)
-        for (int i = 0; i < a.entries; ++i) tops[i * blockDim.x + threadIdx.x] = 0;
-      set_segments<DT>(v, t, seg);
-      __syncthreads();
       if (a.tokens && threadIdx.x == 0)
         x = load_one<DT>(seg.at_column<DT>(v, static_cast<uint32_t>(token)));
       st = row_stats<DT, true, TOP>(v, seg, lo, hi, cta, ctas, slots, phase, tops, a.entry_shift, thread_max);
     }
-    if (threadIdx.x == 0 && cta == 0) {
+    const auto write = [&] {  // once nothing waits for thread 0
+      if (threadIdx.x != 0 || cta != 0) return;
       if (a.tokens) a.log_probs[t] = scored ? st.log_prob(x, v.inv_temp) : 0.f;
       if (a.entropy) a.entropy[t] = st.entropy;
       if (a.stats) {
         a.stats[2 * t] = st.max;
         a.stats[2 * t + 1] = st.log2_s * kLn2;
       }
+    };
+    if (!TOP) {
+      write();
+      continue;
     }
-    if (!TOP) continue;
     const int k = a.top_k;
     float* out_lp = a.top_log_probs + t * k;
     int64_t* out_id = a.top_ids + t * k;
@@ -437,6 +441,7 @@ __global__ void __launch_bounds__(kWarps * 32, TOP ? 4 : 5) log_probs_kernel(con
         out_lp[i] = scored && st.bad() ? NAN : -INFINITY;
         out_id[i] = -1;
       }
+    write();
   }
 }
 

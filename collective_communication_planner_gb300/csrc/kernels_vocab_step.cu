@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(kThreads, kStepCtasPerSm) distill_step_kernel(
       });
     }
     Part p = scan_row<DT, false, true>(v, seg, lo, hi, cta == 0, KeepLoad(), [](float, const Vec<DT>(&)[kBatch]) {});
-    p = row_join(p, c, slots, phase, ctas);
+    p = row_join(p, c, slots, phase, v.step.warps, ctas);
     const Stats st = joined_stats<DT>(p, v, seg, lo, hi, slots, phase, cta, ctas);
     if (cta == 0 && threadIdx.x >= v.step.warps * 32) store_loss(a, t, named, st);
     RowGrad g;

@@ -186,7 +186,7 @@ __device__ __forceinline__ void rebase(Part& a, float m, float c) {
   a.m = m;
 }
 
-// the first `n` (a power of two) lanes' parts joined, the same bits in each of them
+// the parts of every N lanes (a power of two) joined, the same bits in each of them
 template <int N>
 __device__ __forceinline__ Part lanes_join(Part a, float c) {
   float m = a.m;
@@ -201,8 +201,8 @@ __device__ __forceinline__ Part lanes_join(Part a, float c) {
   return a;
 }
 
-constexpr int kMaxWarps = 32;
-constexpr int kMaxCluster = 16;
+constexpr int kMaxWarps = 9;
+constexpr int kMaxCluster = 8;
 
 struct JoinSlots {
   Part warp[2][kMaxWarps];
@@ -236,16 +236,18 @@ __device__ __forceinline__ void remote_store(uint32_t at, uint64_t x) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(x) : "memory");
 }
 
-// Joins the parts of all threads of the cluster; every thread gets the result,
-// the same bits. Slots alternate between two sets: a set is written again two
+// Joins the parts of the streaming warps' threads (eight warps at the most) of
+// all CTAs of the cluster (eight at the most); every thread gets the result, the
+// same bits. Slots alternate between two sets: a set is written again two
 // joins later, past a barrier that every reader of it has reached.
-__device__ __forceinline__ Part row_join(Part a, float c, JoinSlots& slots, int& phase, uint32_t csize) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+__device__ __forceinline__ Part row_join(Part a, float c, JoinSlots& slots, int& phase, uint32_t warps,
+                                         uint32_t csize) {
+  const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31, of8 = lane & 7;
   a = lanes_join<32>(a, c);
   if (lane == 0) slots.warp[phase][warp] = a;
   __syncthreads();
   const Part none{-INFINITY, 0.f, 0.f};
-  a = lanes_join<32>(lane < warps ? slots.warp[phase][lane] : none, c);
+  a = lanes_join<8>(of8 < warps ? slots.warp[phase][of8] : none, c);
   if (csize > 1) {
     if (warp == 0 && lane < csize) {
       const uint32_t at = remote(&slots.cta[phase][cluster_rank()], lane);
@@ -254,7 +256,7 @@ __device__ __forceinline__ Part row_join(Part a, float c, JoinSlots& slots, int&
       remote_store(at + 8, a.u);
     }
     cluster_barrier();
-    a = lanes_join<32>(lane < csize ? slots.cta[phase][lane] : none, c);
+    a = lanes_join<8>(of8 < csize ? slots.cta[phase][of8] : none, c);
   }
   phase ^= 1;
   return a;
