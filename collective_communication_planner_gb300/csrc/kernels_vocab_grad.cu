@@ -21,7 +21,12 @@ struct Item {
   }
 };
 
-
+// y_j = ([j = token] a - p_j (a + b (log p_j + entropy))) / T, elementwise from
+// the forward pass's statistics: 2^(x c - (max c + log2 s)) is one fused operation
+// and one exponential, and (a + b (log p + entropy)) one more fused operation, so
+// that memory bounds it. 48 registers keep five CTAs on an SM, whose loads and
+// stores cover one another. 4096 x 131072 bf16 with entropy, 3072 of them scored,
+// 280 us, 0.99 of the copy rate; 37 x 32003 fp32 is the launch, 4 us.
 template <int DT, bool SLOPE>
 __global__ void __launch_bounds__(kThreads, 5) log_probs_grad_kernel(const __grid_constant__ LogProbsGradArgs a) {
   __shared__ GradSegments seg;
@@ -53,6 +58,11 @@ __global__ void __launch_bounds__(kThreads, 5) log_probs_grad_kernel(const __gri
   }
 }
 
+// y_j = w (Q p_j - q_j) / T, the same way; warp 0 reads the teacher's entries
+// before it joins in, and the columns that they name get their own term behind
+// the body's stores. 1024 x 262144 bf16, 128 entries, 768 of them scored, 153 us,
+// 0.90 of the copy rate: an item's stores wait for Q, two dependent loads and a
+// barrier, which the SM's other CTAs hide but for the first and last items.
 template <int DT>
 __global__ void __launch_bounds__(kThreads, 5) distill_grad_kernel(const __grid_constant__ DistillArgs a) {
   __shared__ GradSegments seg;
@@ -95,11 +105,15 @@ int launch_parts(void (*kernel)(Args), Args& a, VocabLaunch& l) {
   VocabArgs& v = a.v;
   set_cut<DT>(v, v.together ? 0 : 2);
   const auto parts = [](uint32_t chunks, uint32_t share) { return chunks > share ? (chunks + share - 1) / share : 1; };
-  // a short row: a CTA of as many warps as it has chunks
+  // A short row: a CTA of as many warps as it has chunks. GB300, 4096 rows bf16,
+  // so / with eight: 1000 columns 5.5 / 15.0 us, 4000 10.9 / 16.5; from
+  // distillation, 1000 columns 20.8 / 31.0.
   uint32_t warps = kThreads / 32;
   while (warps > 1 && v.cut.chunks <= warps / 2) warps /= 2;
-  // an item is at most eight chunks a warp; fewer where that leaves SMs
-  // without four items
+  // An item is at most eight chunks a warp: 16 / 8 / 4 take 283 / 280 / 278 us for
+  // 4096 x 131072 and, with the teacher's entries read again by every item, 156 /
+  // 153 / 161 for the distillation of 1024 x 262144. Fewer where that leaves SMs
+  // without four items: 16 x 131072 4.5 us, 7.3 in items of eight; 128 rows 10.0, 12.3.
   uint32_t deep = 8;
   while (deep > 1 && v.rows * parts(v.cut.chunks, deep * warps) < static_cast<uint64_t>(l.sm_count) * 4) deep /= 2;
   v.parts = parts(v.cut.chunks, deep * warps);
@@ -112,9 +126,10 @@ int launch_parts(void (*kernel)(Args), Args& a, VocabLaunch& l) {
 }  // namespace
 
 int launch_log_probs_grad(int dtype, LogProbsGradArgs& a, VocabLaunch& l) {
+  const bool slope = a.d_entropy != nullptr;
   if (dtype == kBF16)
-    return launch_parts<kBF16>(a.d_entropy ? log_probs_grad_kernel<kBF16, true> : log_probs_grad_kernel<kBF16, false>, a, l);
-  return launch_parts<kF32>(a.d_entropy ? log_probs_grad_kernel<kF32, true> : log_probs_grad_kernel<kF32, false>, a, l);
+    return launch_parts<kBF16>(slope ? log_probs_grad_kernel<kBF16, true> : log_probs_grad_kernel<kBF16, false>, a, l);
+  return launch_parts<kF32>(slope ? log_probs_grad_kernel<kF32, true> : log_probs_grad_kernel<kF32, false>, a, l);
 }
 
 int launch_distill_grad(int dtype, DistillArgs& a, VocabLaunch& l) {

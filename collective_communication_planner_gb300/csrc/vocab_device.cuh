@@ -367,7 +367,8 @@ __device__ __forceinline__ uint4 load_any(const char* at, Load load) {
 }
 
 template <int DT, typename Load>
-__device__ __forceinline__ void load_vectors(const char* at, uint32_t first, uint32_t end, Vec<DT> (&x)[kBatch], Load load) {
+__device__ __forceinline__ void load_vectors(const char* at, uint32_t first, uint32_t end, Vec<DT> (&x)[kBatch],
+                                             Load load) {
   if (first - (threadIdx.x & 31) + kChunkVectors <= end) {
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) x[k].set(load(at + k * 512));

@@ -210,7 +210,8 @@ __device__ __forceinline__ void store_named(const VocabArgs& v, uint64_t t, cons
 #pragma unroll
     for (int k = 0; k < 32; k += 4) {
       const int4 c = *reinterpret_cast<const int4*>(&e.column[j + k]);
-      same |= (c.x == column) << k | (c.y == column) << (k + 1) | (c.z == column) << (k + 2) | (c.w == column) << (k + 3);
+      same |= (c.x == column) << k | (c.y == column) << (k + 1);
+      same |= (c.z == column) << (k + 2) | (c.w == column) << (k + 3);
     }
     for (; same; same &= same - 1) {
       const int k = j + __ffs(same) - 1;

@@ -371,9 +371,10 @@ tcclResult_t tcclCopyOutInspect(int coll, int nranks, const void* const sendbufs
 
 /*
  * Test hook for the bounded-wait error path: while enabled, each bulk-engine
- * launch (and each launch of tcclDistill's persistent kernel) makes its first CTA wait on a barrier that nothing signals, with a
- * `timeout_ms` bound; the CTA then records tcclDeviceTimeout, skips its
- * remaining work and exits normally (no trap, no fault). Other CTAs finish.
+ * launch (and each launch of tcclDistill's persistent kernel) makes its first
+ * CTA wait on a barrier that nothing signals, with a `timeout_ms` bound; the CTA
+ * then records tcclDeviceTimeout, skips its remaining work and exits normally
+ * (no trap, no fault). Other CTAs finish.
  */
 tcclResult_t tcclGroupInjectWaitTimeout(tcclGroup_t g, int enable, double timeout_ms);
 
