@@ -34,13 +34,24 @@ constexpr uint32_t kSumWarps = 8, kGradWarps = 8;
 constexpr uint32_t kTeacherWarps = 3;  // they take the rows in turn
 constexpr uint32_t kLoaderWarp = kSumWarps + kGradWarps, kFirstTeacher = kLoaderWarp + 1;
 constexpr int kThreads = (kFirstTeacher + kTeacherWarps) * 32;
-// Rows that the ring takes: long ones, since a row's joins and barriers take it
-// about 3 us whatever its bytes (GB300, 4096 rows bf16: 16384 columns 78 us,
-// the kernel that reads twice 63; 32768: 99 and 101; 65536: 175 and 212), several
-// to a cluster (64 rows of 131072: 11.7 and 11.0 us), and not of many short odd
-// segments, whose edge elements one warp does (512 x 50257 over 16 ranks: 47
-// and 23 us).
-constexpr uint32_t kMinChunks = 32, kMinRowsPerCluster = 4, kMaxEdges = 128;
+// Rows that the ring takes, rather than the kernel that reads a row twice. GB300,
+// ring / other, us, bf16 if not said:
+// - long rows, since a row's joins and barriers take it about 3 us whatever its
+//   bytes: 4096 x 16384 78 / 55, 32768 100 / 100, 65536 174 / 206, 131072 351 / 412;
+// - calls that L2 does not keep between the two reads: 256 x 131072 (67 MB) 32.1 /
+//   31.0, 512 x 131072 54.7 / 61.1; 256 x 100003 fp32 (102 MB) 45 / 54, 128 rows
+//   22.5 / 20.8; under a cap, where the other kernel has a CTA to an SM as well,
+//   as soon as a cluster gets a few rows: 8 CTAs, 23 x 131072 42 / 132;
+// - where its warps' rounds over a slice are filled, in bf16, whose arithmetic a
+//   byte is twice fp32's: 4096 x 100003 (0.76 of the rounds) 366 to 458 / 362 to 379,
+//   50257 (0.77) 224 to 260 / 184 to 191, 200001 (0.81) 619 to 689 / 742 to 758;
+//   fp32 1024 x 50257 (0.77) 84 / 97;
+// - not of many short odd segments, whose edge elements one warp does: 512 x 50257
+//   over 16 ranks 47 / 23, 4096 x 131039 over 16 641 / 443.
+constexpr uint32_t kMinChunks = 32, kMaxEdges = 128;
+constexpr uint64_t kMinCtaBytes = 640 << 10;                    // of a call, uncapped
+constexpr uint32_t kMinRowsPerCluster = 4;                      // capped
+constexpr uint64_t kMinFilled = 4, kMinFilledOf = 5;            // 0.8 of the rounds' vectors
 constexpr int kMinSlots = 3, kMaxSlots = 4;
 // What goes with a row within the CTA, row n's being set n % kSets. A teacher
 // warp sets row n + 3's up before it is done with row n, and row n + 6's after
@@ -601,7 +612,15 @@ bool plan_t(DistillArgs& a, VocabLaunch& l) {
   l.cluster = c;
   l.clusters = clusters_that_fit<DT>(c, l);
   if (l.cap > 0 && l.clusters * c > l.cap) l.clusters = l.cap / c;
-  if (v.rows < static_cast<uint64_t>(l.clusters) * kMinRowsPerCluster) return false;
+  if (l.cap > 0) {
+    if (v.rows < static_cast<uint64_t>(l.clusters) * kMinRowsPerCluster) return false;
+  } else {
+    const uint64_t row = v.vocab * static_cast<uint64_t>(Elem<DT>::kBytes);
+    if (v.rows * row < static_cast<uint64_t>(l.clusters) * c * kMinCtaBytes) return false;
+    const uint64_t rounds = ((n + c - 1) / c + kSumWarps - 1) / kSumWarps * kSumWarps;  // chunks' worth, of a CTA
+    const uint64_t vectors = static_cast<uint64_t>(v.used - 1) * v.cut.full + v.cut.last;
+    if (DT == kBF16 && vectors * kMinFilledOf < rounds * c * kChunkVectors * kMinFilled) return false;
+  }
   a.slots = slots(c);
   a.slot_bytes = static_cast<uint32_t>(slot_bytes(c));
   return true;
