@@ -84,8 +84,8 @@ struct RingShared {
   uint64_t full[kMaxSlots];   // a slot's copies have landed (bytes)
   uint64_t empty[kMaxSlots];  // every gradient warp is done with a slot's row
   uint64_t done[kSets];       // every gradient warp has written its share of a row
-  uint64_t joined[kJoins];    // every part of a row is in `part`: this CTA's sum warps' and all
-                              // teacher warps' arrivals, the other sum warps' bytes
+  uint64_t joined[kJoins];    // every part of a row is in `part`: this CTA's arrivals, the others' bytes (with
+                              // `release` their teacher warps' arrivals)
   uint64_t never;             // test hook
   float2 part[kJoins][kRingMaxCluster * kParts];  // maximum and sum
   RingSegments seg[kMaxSlots];
@@ -232,10 +232,18 @@ struct Rows {
   __device__ __forceinline__ uint64_t row(uint32_t n) const { return first + n * step; }
 };
 
-// Sends a sum warp's part of row n, the same in every lane, to every CTA of the
-// cluster. To another CTA: an asynchronous store whose bytes count towards its
-// barrier (a store and a releasing arrival instead waited 1.5 to 2 us behind the
-// gradient warps' stores). To its own, a store and an arrival.
+// Sends a part, the same in every lane, to another CTA of the cluster: an
+// asynchronous store whose bytes count towards its barrier (a store and a
+// releasing arrival instead wait 1.5 to 2 us behind the SM's global stores).
+__device__ __forceinline__ void send_async(const float2* part, const uint64_t* joined, uint32_t to, const Part& p) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(
+                   remote(part, to)),
+               "f"(p.m), "f"(p.s), "r"(remote(joined, to))
+               : "memory");
+}
+
+// A sum warp's part of row n to every CTA of the cluster; to its own, a store
+// and an arrival.
 __device__ __forceinline__ void send_part(RingShared& s, uint32_t n, uint32_t cta, uint32_t ctas, uint32_t warp,
                                           const Part& p) {
   const uint32_t lane = threadIdx.x & 31;
@@ -246,30 +254,31 @@ __device__ __forceinline__ void send_part(RingShared& s, uint32_t n, uint32_t ct
     *part = make_float2(p.m, p.s);
     dev::mbar_arrive(joined);
   } else {
-    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(
-                     remote(part, lane)),
-                 "f"(p.m), "f"(p.s), "r"(remote(joined, lane))
-                 : "memory");
+    send_async(part, joined, lane, p);
   }
 }
 
-// The same for the edge elements' part, by the row's teacher warp: its arrivals
-// release what the warp has written (to its CTA) and read (to the others, which
-// may replace it). The one at the CTA's own barrier says how many bytes the
-// other CTAs' sum warps send.
-__device__ __forceinline__ void send_last_part(RingShared& s, uint32_t n, uint32_t cta, uint32_t ctas, const Part& p) {
+// The edge elements' part, by the row's teacher warp. The arrival at its own
+// CTA's barrier releases what the warp has written and says how many bytes the
+// other CTAs send. To the others a part goes as the sum warps' do or, with
+// `release`, by stores and an arrival that releases the warp's reads: they may
+// replace logits that it has read, in place.
+__device__ __forceinline__ void send_last_part(RingShared& s, uint32_t n, uint32_t cta, uint32_t ctas, bool release,
+                                               const Part& p) {
   const uint32_t lane = threadIdx.x & 31;
   if (lane >= ctas) return;
   float2* part = &s.part[n % kJoins][cta * kParts + kSumWarps];
   uint64_t* joined = &s.joined[n % kJoins];
   if (lane == cta) {
     *part = make_float2(p.m, p.s);
-    dev::mbar_arrive_expect_tx(joined, (ctas - 1) * kSumWarps * 8);
-  } else {
+    dev::mbar_arrive_expect_tx(joined, (ctas - 1) * (release ? kSumWarps : kParts) * 8);
+  } else if (release) {
     const uint32_t at = remote(part, lane);
     remote_store(at, p.m);
     remote_store(at + 4, p.s);
     remote_arrive(joined, lane);
+  } else {
+    send_async(part, joined, lane, p);
   }
 }
 
@@ -480,7 +489,7 @@ __device__ void teacher_warp(const DistillArgs& a, RingShared& s, const Rows& ro
     p = join_lanes_any(p, c);
     if (lane == 0) s.weight[n % kSets] = weight;
     __syncwarp();  // the set, for the release in the arrival at this CTA's barrier
-    send_last_part(s, n, cta, ctas, p);
+    send_last_part(s, n, cta, ctas, a.release, p);
   };
   load(mine);
   begin(mine);
@@ -535,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1) distill_ring_kernel(const __grid_
       dev::mbar_init(&s.empty[i], kGradWarps);
     }
     for (uint32_t i = 0; i < kSets; ++i) dev::mbar_init(&s.done[i], kGradWarps);
-    for (uint32_t i = 0; i < kJoins; ++i) dev::mbar_init(&s.joined[i], kSumWarps + ctas);
+    for (uint32_t i = 0; i < kJoins; ++i) dev::mbar_init(&s.joined[i], kSumWarps + (a.release ? ctas : 1));
     dev::mbar_init(&s.never, 1);
     s.abort = 0;
     dev::fence_mbar_init();
@@ -621,6 +630,11 @@ bool plan_t(DistillArgs& a, VocabLaunch& l) {
     const uint64_t vectors = static_cast<uint64_t>(v.used - 1) * v.cut.full + v.cut.last;
     if (DT == kBF16 && vectors * kMinFilledOf < rounds * c * kChunkVectors * kMinFilled) return false;
   }
+  // Where a gradient replaces its logits the arrivals have to release. In bf16
+  // they do so anyway: GB300, with / without, 4096 x 65536 174 / 177 us, 200001 635 /
+  // 658, 131072 351 / 353; fp32 1024 x 100003 150 / 137, 301 rows 50.6 / 48.5.
+  a.release = DT == kBF16;
+  for (int r = 0; r < v.used; ++r) a.release |= v.p.dst[r] == v.p.src[r];
   a.slots = slots(c);
   a.slot_bytes = static_cast<uint32_t>(slot_bytes(c));
   return true;

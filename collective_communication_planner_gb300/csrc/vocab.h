@@ -74,6 +74,7 @@ struct DistillArgs {
   // ring kernel: shared-memory slots for a CTA's slices of rows, bounded waits
   int slots;
   uint32_t slot_bytes;
+  int release;  // teacher warps' arrivals release their reads
   ChunkStep sum_step, grad_step;  // of its two kinds of warps
   int* status;
   uint64_t timeout_ns;
