@@ -13,7 +13,7 @@
 //
 // loss = sum_k q_k (log q_k - z_k + lse), y_j = w (Q p_j - q_j) / T: two
 // exponentials an element, one for the sum, one for the gradient. 4096 x 131072
-// bf16, 64 entries: 350 us, 0.91 of the copy rate for one read and one write (the
+// bf16, 64 entries: 352 us, 0.90 of the copy rate for one read and one write (the
 // kernel that reads a row twice: 468). Bound by memory, on 144 of 152 SMs: three
 // slots of a row's slice want clusters of four. Streaming warps, sums and
 // gradients: 8 + 8 345 us, 10 + 10 360, 12 + 12 362, 6 + 8 359, 8 + 10 363; more
