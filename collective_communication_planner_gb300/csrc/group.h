@@ -89,7 +89,7 @@ struct tcclGroup {
   std::map<tccl::PlanKey, std::unique_ptr<tccl::CachedPlan>> plans;
   std::map<std::string, std::unique_ptr<tccl::CachedReshard>> reshards;
   // distillation ring: clusters of each size that fit on the device at once
-  int ring_clusters[2 * (tccl::kRingMaxCluster + 1)] = {};
+  int ring_clusters[4 * (tccl::kRingMaxCluster + 1)] = {};
   tcclLaunchInfo_t last;
   // copy-out engine: the group's own copy streams and the events that order
   // them after each segment's kernel and join them back to the caller

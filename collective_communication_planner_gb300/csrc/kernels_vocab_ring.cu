@@ -13,8 +13,8 @@
 //
 // loss = sum_k q_k (log q_k - z_k + lse), y_j = w (Q p_j - q_j) / T: two
 // exponentials an element, one for the sum, one for the gradient. 4096 x 131072
-// bf16, 64 entries: 352 us, 0.90 of the copy rate for one read and one write (the
-// kernel that reads a row twice: 468). Bound by memory, on 144 of 152 SMs: three
+// bf16, 64 entries: 342 us, 0.93 of the copy rate for one read and one write (the
+// kernel that reads a row twice: 412). Bound by memory, on 144 of 152 SMs: three
 // slots of a row's slice want clusters of four. Streaming warps, sums and
 // gradients: 8 + 8 345 us, 10 + 10 360, 12 + 12 362, 6 + 8 359, 8 + 10 363; more
 // of them share a slice's chunks less evenly and keep the other warps from issuing.
@@ -37,7 +37,8 @@ constexpr int kThreads = (kFirstTeacher + kTeacherWarps) * 32;
 // Rows that the ring takes, rather than the kernel that reads a row twice. GB300,
 // ring / other, us, bf16 if not said:
 // - long rows, since a row's joins and barriers take it about 3 us whatever its
-//   bytes: 4096 x 16384 78 / 55, 32768 100 / 100, 65536 174 / 206, 131072 351 / 412;
+//   bytes: 4096 x 16384 78 / 55, 32768 104 / 100, 65536 173 / 206, 131072 342 / 412,
+//   1024 x 32768 fp32 52 / 60;
 // - calls that L2 does not keep between the two reads: 256 x 131072 (67 MB) 32.1 /
 //   31.0, 512 x 131072 54.7 / 61.1; 256 x 100003 fp32 (102 MB) 45 / 54, 128 rows
 //   22.5 / 20.8; under a cap, where the other kernel has a CTA to an SM as well,
@@ -46,9 +47,10 @@ constexpr int kThreads = (kFirstTeacher + kTeacherWarps) * 32;
 //   byte is twice fp32's: 4096 x 100003 (0.76 of the rounds) 366 to 458 / 362 to 379,
 //   50257 (0.77) 224 to 260 / 184 to 191, 200001 (0.81) 619 to 689 / 742 to 758;
 //   fp32 1024 x 50257 (0.77) 84 / 97;
-// - not of many short odd segments, whose edge elements one warp does: 512 x 50257
+// - in bf16 with edge elements, which one warp does, longer ones: 4096 x 65529
+//   226 / 209, 131065 409 / 415; and not of many short odd segments: 512 x 50257
 //   over 16 ranks 47 / 23, 4096 x 131039 over 16 641 / 443.
-constexpr uint32_t kMinChunks = 32, kMaxEdges = 128;
+constexpr uint32_t kMinCappedChunks = 32, kMinChunks = 48, kMinEdgedChunks = 96, kMaxEdges = 128;
 constexpr uint64_t kMinCtaBytes = 640 << 10;                    // of a call, uncapped
 constexpr uint32_t kMinRowsPerCluster = 4;                      // capped
 constexpr uint64_t kMinFilled = 4, kMinFilledOf = 5;            // 0.8 of the rounds' vectors
@@ -57,7 +59,7 @@ constexpr int kMinSlots = 3, kMaxSlots = 4;
 // warp sets row n + 3's up before it is done with row n, and row n + 6's after
 // that: every warp that reads row n's set is past it then.
 constexpr uint32_t kSets = 2 * kTeacherWarps;
-constexpr uint32_t kEdgeBatch = 4;  // edge elements whose loads a lane issues together
+constexpr uint32_t kEdgeBatch = kMaxEdges / 32;  // edge elements of a lane
 // The parts of a row, row n's being set n % kJoins: from every CTA of the
 // cluster the sum warps' and, as the last, the edge elements' from the row's
 // teacher warp. A warp of another CTA sends row n only when all have sent row
@@ -436,19 +438,25 @@ __device__ __forceinline__ uint32_t edge_column(const VocabArgs& v, uint64_t t, 
   return seg * v.shard + col;
 }
 
-template <int DT>
+// EDGES: the rows have edge elements, whose code the teacher warps of others do
+// without (GB300, 4096 x 131072 bf16: 342 us, 353 with it). They are read with the
+// entries' logits: read where they are used, twice, 4096 x 65529 took 253 us for
+// 226, 131065 425 for 409 (but 1024 x 50257 fp32 85 for 92).
+template <int DT, bool EDGES>
 __device__ void teacher_warp(const DistillArgs& a, RingShared& s, const Rows& rows, uint32_t cta, uint32_t ctas,
                              uint32_t lo, uint32_t hi, const Wait& wait) {
   const VocabArgs& v = a.v;
   const float c = v.exp2_scale;
   const uint32_t lane = threadIdx.x & 31, mine = (threadIdx.x >> 5) - kFirstTeacher;
   // A row's loads are issued an iteration (three rows) before they are used:
-  // its entries, then the logits at their columns. `entries` and `weight` are the
-  // next row's to be begun, q and x the one's begun.
+  // its entries, then the logits at their columns and the edge elements. `entries`
+  // and `next_weight` are the next row's to be begun, q, x, weight and edge the
+  // one's begun.
   TeacherEntries entries;
   TeacherRow q;
   uint32_t x[kMaxTop / 32];
-  float weight = 0.f, next_weight = 0.f;
+  float weight = 0.f, next_weight = 0.f, edge[kEdgeBatch];
+  const uint32_t edges = EDGES && cta == 0 ? v.cut.edges : 0;
   const auto load = [&](uint32_t n) {
     if (n >= rows.count) return;
     entries = load_teacher(a, rows.row(n));
@@ -459,34 +467,35 @@ __device__ void teacher_warp(const DistillArgs& a, RingShared& s, const Rows& ro
     q = teacher_row(a, entries);
     weight = next_weight * v.inv_temp;
     load_named<DT>(v, rows.row(n), q, x);
+    if (!EDGES) return;
+#pragma unroll
+    for (uint32_t i = 0; i < kEdgeBatch; ++i) {
+      const uint32_t e = lane + 32 * i;
+      edge[i] = e < edges ? read_column<DT>(v, rows.row(n), edge_column<DT>(v, rows.row(n), e)) : -INFINITY;
+    }
   };
   // The row's set is complete and, with the edge elements' part as the last of
   // the row's parts, the row may go to the other CTAs: all that they replace of
   // it, in place, has been read.
   const auto finish = [&](uint32_t n) {
     if (n >= rows.count) return;
-    const uint64_t t = rows.row(n);
     set_entries<DT>(q, x, a.top_k, s.named[n % kSets], [&](uint32_t column) {
-      return has_column<DT>(v, t, column, lo, hi, cta == 0);
+      return has_column<DT>(v, rows.row(n), column, lo, hi, cta == 0);
     });
     Part p{-INFINITY, 0.f, 0.f};
-    if (cta == 0) {
-      for (uint32_t e = lane; e < v.cut.edges; e += 32 * kEdgeBatch) {
-        float y[kEdgeBatch];
+    if (EDGES) {
 #pragma unroll
-        for (uint32_t i = 0; i < kEdgeBatch; ++i)
-          y[i] = e + 32 * i < v.cut.edges ? read_column<DT>(v, t, edge_column<DT>(v, t, e + 32 * i)) : -INFINITY;
-#pragma unroll
-        for (uint32_t i = 0; i < kEdgeBatch; ++i) {
-          if (y[i] > p.m) {
-            p.s *= exp2_ftz((p.m - y[i]) * c);
-            p.m = y[i];
-          }
-          if (y[i] != -INFINITY) p.s += exp2_ftz((y[i] - (p.m == -INFINITY ? 0.f : p.m)) * c);
+      for (uint32_t i = 0; i < kEdgeBatch; ++i) {
+        if (32 * i >= edges) break;
+        const float y = edge[i];
+        if (y > p.m) {
+          p.s *= exp2_ftz((p.m - y) * c);
+          p.m = y;
         }
+        if (y != -INFINITY) p.s += exp2_ftz((y - (p.m == -INFINITY ? 0.f : p.m)) * c);
       }
+      p = join_lanes_any(p, c);
     }
-    p = join_lanes_any(p, c);
     if (lane == 0) s.weight[n % kSets] = weight;
     __syncwarp();  // the set, for the release in the arrival at this CTA's barrier
     send_last_part(s, n, cta, ctas, a.release, p);
@@ -497,6 +506,9 @@ __device__ void teacher_warp(const DistillArgs& a, RingShared& s, const Rows& ro
   finish(mine);
   for (uint32_t n = mine; n < rows.count; n += kTeacherWarps) {
     const uint64_t t = rows.row(n);
+    float held[kEdgeBatch];  // this row's
+#pragma unroll
+    for (uint32_t i = 0; i < kEdgeBatch; ++i) held[i] = edge[i];
     begin(n + kTeacherWarps);
     load(n + 2 * kTeacherWarps);
     if (!wait(&s.joined[n % kJoins], n / kJoins)) return;
@@ -508,15 +520,10 @@ __device__ void teacher_warp(const DistillArgs& a, RingShared& s, const Rows& ro
     g.zero = w == 0.f || named.total == 0.f || st.empty();
     if (cta == 0) {
       store_loss(a, t, named, st);
-      for (uint32_t e = lane; e < v.cut.edges; e += 32 * kEdgeBatch) {
-        float y[kEdgeBatch];
 #pragma unroll
-        for (uint32_t i = 0; i < kEdgeBatch; ++i)
-          if (e + 32 * i < v.cut.edges) y[i] = read_column<DT>(v, t, edge_column<DT>(v, t, e + 32 * i));
-#pragma unroll
-        for (uint32_t i = 0; i < kEdgeBatch; ++i)
-          if (e + 32 * i < v.cut.edges)
-            write_column<DT>(v, t, edge_column<DT>(v, t, e + 32 * i), g.zero ? 0.f : g.one(y[i]));
+      for (uint32_t i = 0; i < kEdgeBatch; ++i) {
+        const uint32_t e = lane + 32 * i;
+        if (EDGES && e < edges) write_column<DT>(v, t, edge_column<DT>(v, t, e), g.zero ? 0.f : g.one(held[i]));
       }
     }
     finish(n + kTeacherWarps);
@@ -529,7 +536,7 @@ __device__ void teacher_warp(const DistillArgs& a, RingShared& s, const Rows& ro
   }
 }
 
-template <int DT>
+template <int DT, bool EDGES>
 __global__ void __launch_bounds__(kThreads, 1) distill_ring_kernel(const __grid_constant__ DistillArgs a) {
   extern __shared__ __align__(128) unsigned char dynamic[];
   RingShared& s = *reinterpret_cast<RingShared*>(dynamic);
@@ -561,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1) distill_ring_kernel(const __grid_
   if (warp < kSumWarps) sum_warp<DT>(a, s, ring, rows, cta, ctas, lo, hi, wait);
   else if (warp < kLoaderWarp) grad_warp<DT>(a, s, ring, rows, cta, ctas, lo, hi, wait);
   else if (warp == kLoaderWarp) loader_warp<DT>(a, s, ring, rows, lo, hi, wait);
-  else teacher_warp<DT>(a, s, rows, cta, ctas, lo, hi, wait);
+  else teacher_warp<DT, EDGES>(a, s, rows, cta, ctas, lo, hi, wait);
   __syncwarp();
   if (ctas > 1) cluster_barrier();
 }
@@ -569,8 +576,8 @@ __global__ void __launch_bounds__(kThreads, 1) distill_ring_kernel(const __grid_
 // How many clusters of this size run at once, a CTA to an SM: asked once a
 // group, 0 if the device cannot say.
 template <int DT>
-int clusters_that_fit(int cluster, VocabLaunch& l) {
-  int& fit = l.ring_clusters[(DT == kBF16 ? 1 : 0) * (kRingMaxCluster + 1) + cluster];
+int clusters_that_fit(int cluster, bool edges, VocabLaunch& l) {
+  int& fit = l.ring_clusters[((DT == kBF16 ? 2 : 0) + edges) * (kRingMaxCluster + 1) + cluster];
   if (fit > 0) return fit;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(cluster));
@@ -583,9 +590,10 @@ int clusters_that_fit(int cluster, VocabLaunch& l) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaFuncSetAttribute(distill_ring_kernel<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  const auto kernel = edges ? distill_ring_kernel<DT, true> : distill_ring_kernel<DT, false>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(l.smem_optin)) != cudaSuccess ||
-      cudaOccupancyMaxActiveClusters(&fit, distill_ring_kernel<DT>, &cfg) != cudaSuccess) {
+      cudaOccupancyMaxActiveClusters(&fit, kernel, &cfg) != cudaSuccess) {
     fit = 0;
     cudaGetLastError();
   }
@@ -597,7 +605,7 @@ bool plan_t(DistillArgs& a, VocabLaunch& l) {
   VocabArgs& v = a.v;
   set_cut<DT>(v, v.together ? 0 : 2);
   const uint32_t n = v.cut.chunks;
-  if (n < kMinChunks || v.cut.edges > kMaxEdges || l.smem_optin < kSharedBytes) return false;
+  if (n < kMinCappedChunks || v.cut.edges > kMaxEdges || l.smem_optin < kSharedBytes) return false;
   const size_t room = l.smem_optin - kSharedBytes;
   const auto slot_bytes = [&](int c) {
     return static_cast<size_t>((n + c - 1) / c) * (kChunkVectors * 16) + v.used * 16;
@@ -611,7 +619,7 @@ bool plan_t(DistillArgs& a, VocabLaunch& l) {
   int c = 0, most = 0;
   for (int k = 1; k <= kRingMaxCluster && (l.cap <= 0 || k <= l.cap); ++k) {
     if (slots(k) < kMinSlots) continue;
-    const int n_ctas = k * clusters_that_fit<DT>(k, l);
+    const int n_ctas = k * clusters_that_fit<DT>(k, v.cut.edges > 0, l);
     if (n_ctas > most) {
       most = n_ctas;
       c = k;
@@ -619,7 +627,7 @@ bool plan_t(DistillArgs& a, VocabLaunch& l) {
   }
   if (c == 0) return false;
   l.cluster = c;
-  l.clusters = clusters_that_fit<DT>(c, l);
+  l.clusters = clusters_that_fit<DT>(c, v.cut.edges > 0, l);
   if (l.cap > 0 && l.clusters * c > l.cap) l.clusters = l.cap / c;
   if (l.cap > 0) {
     if (v.rows < static_cast<uint64_t>(l.clusters) * kMinRowsPerCluster) return false;
@@ -629,6 +637,7 @@ bool plan_t(DistillArgs& a, VocabLaunch& l) {
     const uint64_t rounds = ((n + c - 1) / c + kSumWarps - 1) / kSumWarps * kSumWarps;  // chunks' worth, of a CTA
     const uint64_t vectors = static_cast<uint64_t>(v.used - 1) * v.cut.full + v.cut.last;
     if (DT == kBF16 && vectors * kMinFilledOf < rounds * c * kChunkVectors * kMinFilled) return false;
+    if (n < (DT == kBF16 && v.cut.edges ? kMinEdgedChunks : kMinChunks)) return false;
   }
   // Where a gradient replaces its logits the arrivals have to release. In bf16
   // they do so anyway: GB300, with / without, 4096 x 65536 174 / 177 us, 200001 635 /
@@ -645,7 +654,8 @@ int launch_t(DistillArgs& a, VocabLaunch& l) {
   a.sum_step = step_of(a.v.cut, kSumWarps);
   a.grad_step = step_of(a.v.cut, kGradWarps);
   // all the shared memory, so that one CTA has an SM to itself
-  return launch_rows(distill_ring_kernel<DT>, a, l, static_cast<uint64_t>(l.clusters) * l.cluster, kThreads, l.cluster,
+  const auto kernel = a.v.cut.edges ? distill_ring_kernel<DT, true> : distill_ring_kernel<DT, false>;
+  return launch_rows(kernel, a, l, static_cast<uint64_t>(l.clusters) * l.cluster, kThreads, l.cluster,
                      l.smem_optin);
 }
 

@@ -87,7 +87,7 @@ struct VocabLaunch {
   int sm_count, cap;
   size_t smem_optin;
   void* stream;
-  int* ring_clusters;  // the group's cache: [dtype][cluster size], clusters that fit at once (0: not asked yet)
+  int* ring_clusters;  // the group's cache: [dtype][edges][cluster size], clusters that fit at once (0: not asked yet)
   int cluster, clusters;  // plan_distill_ring's
   int ctas, threads;      // out
 };
