@@ -51,9 +51,9 @@ constexpr int kThreads = (kFirstTeacher + kTeacherWarps) * 32;
 //   226 / 209, 131065 409 / 415; and not of many short odd segments: 512 x 50257
 //   over 16 ranks 47 / 23, 4096 x 131039 over 16 641 / 443.
 constexpr uint32_t kMinCappedChunks = 32, kMinChunks = 48, kMinEdgedChunks = 96, kMaxEdges = 128;
-constexpr uint64_t kMinCtaBytes = 640 << 10;                    // of a call, uncapped
-constexpr uint32_t kMinRowsPerCluster = 4;                      // capped
-constexpr uint64_t kMinFilled = 4, kMinFilledOf = 5;            // 0.8 of the rounds' vectors
+constexpr uint64_t kMinCtaBytes = 640 << 10;          // of a call, uncapped
+constexpr uint32_t kMinRowsPerCluster = 4;            // capped
+constexpr uint64_t kMinFilled = 4, kMinFilledOf = 5;  // 0.8 of the rounds' vectors
 constexpr int kMinSlots = 3, kMaxSlots = 4;
 // What goes with a row within the CTA, row n's being set n % kSets. A teacher
 // warp sets row n + 3's up before it is done with row n, and row n + 6's after
